@@ -25,7 +25,7 @@ def listed():
     return [
         # one decode token of a layer of 512 experts: latency is all that counts
         dict(name="route_decode", op=ROUTE, T=1, E=512, k=10, score="sigmoid", bias=True, G=8, top=4, gtop=2,
-             renorm=True, scale=2.5, L=0.15),
+             renorm=True, scale=2.5, L=0.125),
         # a prefill chunk, sigmoid scores with the balancing bias, half of the groups kept
         dict(name="route_chunk", op=ROUTE, T=4096, E=256, k=8, score="sigmoid", bias=True, G=8, top=4, gtop=2,
              renorm=True, scale=2.5, L=0.0),
@@ -69,7 +69,7 @@ def draw(rng):
         T = _log(rng, 1, min(16384, 16384 * 512 // E))
         return dict(op=op, T=T, E=E, k=k, score=rng.choice(["softmax", "sigmoid"]), bias=rng.random() < 0.7, G=G,
                     top=top, gtop=rng.randint(1, 2), renorm=rng.random() < 0.7, scale=rng.choice([1.0, 2.5]),
-                    L=rng.choice([0.0, 0.0, 0.15]))
+                    L=rng.choice([0.0, 0.0, 0.125]))
     if op in (NORM, QUANT):
         H, h, delta = 8 * _log(rng, 2, 1024), rng.choice(["bf16", "f32"]), rng.choice(["none", "bf16", "f32"])
         wide = (h == "f32") + (op == NORM and delta == "f32")  # rows of fp32: fewer of them
