@@ -359,6 +359,113 @@ moe_status moe_quantize_rows(const float* w, int32_t rows, int32_t K, int32_t gr
 moe_status moe_router_logits(const uint16_t* x, int32_t T, const uint16_t* W, const float* bias, float scale,
                              int32_t E, int32_t H, float* logits, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the routed experts: routers with biased or grouped
+ * scores, the norm in front of the layer, and an always-on expert of its own
+ * width in 8-bit integers (the routed experts stream, the shared expert stays
+ * resident: BigMoeOnEdge docs/limitations.md, "Limitations").  They keep no
+ * state and take no workspace: any number of calls may run at once, on any
+ * streams and in any captured graphs, as long as their buffers are their own.
+ * Outputs may not overlap inputs except where a call says so.
+ * ---------------------------------------------------------------------- */
+
+/* Element types of the calls below. */
+enum { MOE_BF16 = 0, MOE_F32 = 1 };
+
+/* How moe_route_grouped scores and chooses. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+typedef struct {
+  int32_t score;       /* MOE_SCORE_*: s = softmax(l) over all E experts, or sigmoid(l) each */
+  int32_t n_groups;    /* experts form n_groups groups of E / n_groups consecutive ids (1..32) */
+  int32_t top_groups;  /* groups a token may choose from (1..n_groups; n_groups: no limit) */
+  int32_t group_top;   /* a group's score: its best choice score (1), or the sum of its best two (2) */
+  int32_t renormalise; /* != 0: the chosen experts' scores are divided by their sum */
+  float scale;         /* factor of every weight */
+} moe_route_config;
+
+/* Stage 1 for routers with biased or grouped scores: the counterpart of
+ * moe_route and moe_route_shared, whose outputs moe_sort takes the same way.
+ * For each token, over reals (equal values go to the lower id or group):
+ *   s_e = softmax(l)_e or sigmoid(l_e);  c_e = s_e + bias_e
+ *   L > 0: c_e += L (max c - min c) for resident e (the cache-aware
+ *     substitution of moe_route, in the score that chooses)
+ *   the top_groups groups by the sum of their group_top best c are kept
+ *   ids: the k best of the kept groups by (c desc, l desc, e asc)
+ *   w_j = scale s_e, or scale s_e / sum of the chosen s (renormalise; 0 where
+ *     that sum is 0)
+ * The choice is made in 64-bit arithmetic or proved equal to it.
+ *   logits     device fp32 [T, E].  -inf (or NaN) turns an expert off for the
+ *              token: its c is -inf and its s 0, so it is chosen, with weight
+ *              0, only when the kept groups have no other expert left
+ *   bias       device fp32 [E], finite, or NULL
+ *   slot_table as moe_route; with n_shared > 0 its first E entries are read
+ *   n_shared, shared_w  as moe_route_shared: ids E.. and their weights after
+ *              each token's top-k
+ *   ids, w     device int32 / fp32 [T, k + n_shared]
+ * d gives E and k.  MOE_ERR_INVALID: E not a multiple of n_groups, k more
+ * than the kept groups hold, group_top more than a group holds.
+ * MOE_ERR_UNSUPPORTED: more than 32 groups. */
+moe_status moe_route_grouped(const float* logits, int32_t T, const moe_layer_desc* d, const moe_route_config* c,
+                             const float* bias, float L, const int32_t* slot_table, int32_t n_shared,
+                             const float* shared_w, int32_t* ids, float* w, cudaStream_t stream);
+
+/* Residual sum, root-mean-square norm and 8-bit codes of every row:
+ *   h' = h + delta in fp32, rounded to h's type (delta NULL: h' = h)
+ *   r = 1 / sqrt(mean h'^2 + eps);  x = bf16(h' r gamma)
+ *   p = h' gamma (fp32), a = max |p|:  q = rint(127 p / a), ties to even, and
+ *   q_scale = a r / 127, so that q q_scale stands for h' r gamma
+ *   h       device [T, H] of h_type (MOE_BF16 or MOE_F32)
+ *   delta   device [T, H] of delta_type, or NULL
+ *   gamma   device bf16 [H];  eps > 0
+ *   h_out   device [T, H] of h_type (may be h itself), or NULL
+ *   x       device bf16 [T, H] (what moe_router_logits and moe_expert_ffn
+ *           read), or NULL
+ *   q, q_scale  device int8 [T, H] and fp32 [T] (what moe_int_matmul reads),
+ *           or both NULL; x or q must be given
+ * A row of zeros has codes and scale 0; a row with an infinity or a NaN has
+ * codes 0 and scale NaN.  Squares are summed in fp32 in a fixed order
+ * (deterministic); |h'| below 1e18.  H a multiple of 8, at most 65536; h,
+ * delta, gamma, h_out and x 16-byte aligned, q 8-byte aligned. */
+moe_status moe_add_norm_quant(const void* h, int32_t h_type, const void* delta, int32_t delta_type,
+                              const uint16_t* gamma, float eps, int32_t T, int32_t H, void* h_out, uint16_t* x,
+                              int8_t* q, float* q_scale, cudaStream_t stream);
+
+/* 8-bit codes of plain rows, one scale per row: a = max |w|,
+ * q = rint(127 w / a), ties to even, scale = a / 127.  For the output
+ * channels of weights (once, when a model is loaded) and for activations that
+ * no norm precedes.
+ *   w      device [rows, K] of w_type, 16-byte aligned; K a multiple of 8, at
+ *          most 65536
+ *   q      device int8 [rows, K], 8-byte aligned;  scale  device fp32 [rows]
+ * Rows of zeros and rows with an infinity or a NaN as moe_add_norm_quant. */
+moe_status moe_quantize_channels(const void* w, int32_t w_type, int32_t rows, int32_t K, int8_t* q, float* scale,
+                                 cudaStream_t stream);
+
+/* SwiGLU with 8-bit codes: v = silu(gate) up in fp32, a = max |v| of the row,
+ * q = rint(127 v / a), q_scale = a / 127.
+ *   gu     device [T, 2I] of gu_type: a row's I gate values, then its I up
+ *          values; 16-byte aligned; I a multiple of 8, at most 65536
+ *   q      device int8 [T, I], 8-byte aligned;  q_scale  device fp32 [T]
+ * Rows of zeros and rows with an infinity or a NaN as moe_add_norm_quant. */
+moe_status moe_swiglu_quant(const void* gu, int32_t gu_type, int32_t T, int32_t I, int8_t* q, float* q_scale,
+                            cudaStream_t stream);
+
+/* Product of 8-bit integer rows with a scale per token and per output:
+ *   y[t][n] = add[t][n] + row_w[t] x_scale[t] w_scale[n] sum_k xq[t][k] wq[n][k]
+ * The sum is accumulated in int32, exactly; the rest is fp32, rounded once
+ * more where y is bf16.
+ *   xq, x_scale  device int8 [T, K], 16-byte aligned, and fp32 [T]
+ *   wq, w_scale  device int8 [N, K], 16-byte aligned, and fp32 [N]
+ *   add          device fp32 [T, N] or NULL; may be y where y is fp32 (an
+ *                always-on expert added to the routed experts' sum)
+ *   row_w        device fp32 [T] (a per-token gate) or NULL (1)
+ *   y            device [T, N] of y_type (MOE_BF16 or MOE_F32)
+ *   dev_err      device int32 [1] (MOE_DEV_ERR_TIMEOUT) or NULL
+ * K a multiple of 16, at most 65536; T and N at most 2^20 (no work for 0). */
+moe_status moe_int_matmul(const int8_t* xq, const float* x_scale, int32_t T, const int8_t* wq, const float* w_scale,
+                          int32_t N, int32_t K, const float* add, const float* row_w, void* y, int32_t y_type,
+                          int32_t* dev_err, cudaStream_t stream);
+
 /* Test: the fp32 exp used by moe_route, elementwise on n device floats. */
 moe_status moe_exp_portable(const float* x, int64_t n, float* out, cudaStream_t stream);
 

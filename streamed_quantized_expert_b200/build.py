@@ -20,6 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 SO = os.path.join(HERE, "libmoe.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "route_sort.cu", "router.cu", "quant.cu", "ffn_decode.cu", "ffn_fused.cu", "prefill_tc.cu", "noalloc.cu",
+           "route_grouped.cu", "row_quant.cu", "int_matmul.cu",
            "slot_cache.cpp", "driver.cpp"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [

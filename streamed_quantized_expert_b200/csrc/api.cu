@@ -27,6 +27,22 @@ moe_status check_desc(const moe_layer_desc* d) {
   return MOE_OK;
 }
 
+bool type_ok(int32_t t) { return t == MOE_BF16 || t == MOE_F32; }
+
+// d has passed check_desc.
+moe_status check_route_config(const moe_layer_desc* d, const moe_route_config* c) {
+  if (!c) return MOE_ERR_INVALID;
+  if (c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID;
+  if (c->n_groups < 1 || d->E % c->n_groups || c->top_groups < 1 || c->top_groups > c->n_groups) return MOE_ERR_INVALID;
+  const int m = d->E / c->n_groups;  // experts of a group
+  if (c->group_top < 1 || c->group_top > 2 || (c->top_groups < c->n_groups && c->group_top > m))
+    return MOE_ERR_INVALID;
+  if (d->k > c->top_groups * m) return MOE_ERR_INVALID;
+  if (!(c->scale >= -1e30f && c->scale <= 1e30f)) return MOE_ERR_INVALID;
+  if (c->n_groups > kRouteMaxGroups) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 thread_local const char* g_last_cuda_error = "no error";
 
 std::atomic<long long> g_wait_limit{kDefaultWaitCycles};
@@ -390,6 +406,119 @@ moe_status moe_router_logits(const uint16_t* x, int32_t T, const uint16_t* W, co
   if (!x || !W || !logits || !aligned(x, 16) || !aligned(W, 16)) return MOE_ERR_INVALID;
   if (T > 65535) return MOE_ERR_UNSUPPORTED;
   return cuda_status(launch_router(x, W, bias, scale, T, E, H, logits, stream));
+}
+
+moe_status moe_route_grouped(const float* logits, int32_t T, const moe_layer_desc* d, const moe_route_config* c,
+                             const float* bias, float L, const int32_t* slot_table, int32_t n_shared,
+                             const float* shared_w, int32_t* ids, float* w, cudaStream_t stream) {
+  moe_status s = check_desc(d);
+  if (s != MOE_OK) return s;
+  s = check_route_config(d, c);
+  if (s != MOE_OK) return s;
+  if (T < 0 || !(L >= 0.0f) || L > 1e30f || n_shared < 0 || n_shared > kMaxShared) return MOE_ERR_INVALID;
+  if (T == 0) return MOE_OK;
+  if (!logits || !ids || !w) return MOE_ERR_INVALID;
+  if (L > 0.0f && !slot_table) return MOE_ERR_INVALID;
+  if ((int64_t)T * d->k > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  RouteGroupedArgs a{};
+  a.logits = logits;
+  a.T = T;
+  a.E = d->E;
+  a.k = d->k;
+  a.G = c->n_groups;
+  a.top = c->top_groups;
+  a.gtop = c->group_top;
+  a.sigmoid = c->score == MOE_SCORE_SIGMOID;
+  a.renorm = c->renormalise != 0;
+  a.scale = c->scale;
+  a.bias = bias;
+  a.L = L;
+  a.table = slot_table;
+  a.ns = n_shared;
+  a.shared_w = shared_w;
+  a.ids = ids;
+  a.w = w;
+  return cuda_status(launch_route_grouped(a, stream));
+}
+
+moe_status moe_quantize_channels(const void* w, int32_t w_type, int32_t rows, int32_t K, int8_t* q, float* scale,
+                                 cudaStream_t stream) {
+  if (rows < 0 || K < 8 || K % 8 || !type_ok(w_type)) return MOE_ERR_INVALID;
+  if (K > 1 << 16) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!w || !q || !scale || !aligned(w, 16) || !aligned(q, 8) || !aligned(scale, 4)) return MOE_ERR_INVALID;
+  RowQuantArgs a{};
+  a.in = w;
+  a.H = K;
+  a.q = q;
+  a.scale = scale;
+  return cuda_status(launch_row_quant(a, kRowPlain, w_type == MOE_F32, false, rows, stream));
+}
+
+moe_status moe_add_norm_quant(const void* h, int32_t h_type, const void* delta, int32_t delta_type,
+                              const uint16_t* gamma, float eps, int32_t T, int32_t H, void* h_out, uint16_t* x,
+                              int8_t* q, float* q_scale, cudaStream_t stream) {
+  if (T < 0 || H < 8 || H % 8 || !type_ok(h_type) || (delta && !type_ok(delta_type))) return MOE_ERR_INVALID;
+  if (!(eps > 0.0f) || eps > 1e30f) return MOE_ERR_INVALID;
+  if (H > 1 << 16) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!h || !gamma || (!x && !q) || !q != !q_scale) return MOE_ERR_INVALID;
+  if (!aligned(h, 16) || !aligned(delta, 16) || !aligned(gamma, 16) || !aligned(h_out, 16) || !aligned(x, 16) ||
+      !aligned(q, 8) || !aligned(q_scale, 4))
+    return MOE_ERR_INVALID;
+  RowQuantArgs a{};
+  a.in = h;
+  a.delta = delta;
+  a.gamma = gamma;
+  a.eps = eps;
+  a.H = H;
+  a.h_out = h_out;
+  a.x = x;
+  a.q = q;
+  a.scale = q_scale;
+  return cuda_status(launch_row_quant(a, kRowNorm, h_type == MOE_F32, delta && delta_type == MOE_F32, T, stream));
+}
+
+moe_status moe_swiglu_quant(const void* gu, int32_t gu_type, int32_t T, int32_t I, int8_t* q, float* q_scale,
+                            cudaStream_t stream) {
+  if (T < 0 || I < 8 || I % 8 || !type_ok(gu_type)) return MOE_ERR_INVALID;
+  if (I > 1 << 16) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!gu || !q || !q_scale || !aligned(gu, 16) || !aligned(q, 8) || !aligned(q_scale, 4)) return MOE_ERR_INVALID;
+  RowQuantArgs a{};
+  a.in = gu;
+  a.H = I;
+  a.q = q;
+  a.scale = q_scale;
+  return cuda_status(launch_row_quant(a, kRowSwiglu, gu_type == MOE_F32, false, T, stream));
+}
+
+moe_status moe_int_matmul(const int8_t* xq, const float* x_scale, int32_t T, const int8_t* wq, const float* w_scale,
+                          int32_t N, int32_t K, const float* add, const float* row_w, void* y, int32_t y_type,
+                          int32_t* dev_err, cudaStream_t stream) {
+  if (T < 0 || N < 0 || K < 16 || K % 16 || !type_ok(y_type)) return MOE_ERR_INVALID;
+  if (T > 1 << 20 || N > 1 << 20 || K > 1 << 16) return MOE_ERR_UNSUPPORTED;
+  if (T == 0 || N == 0) return MOE_OK;
+  if (!xq || !x_scale || !wq || !w_scale || !y || !aligned(xq, 16) || !aligned(wq, 16)) return MOE_ERR_INVALID;
+  if (!aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(add, 4) || !aligned(row_w, 4) ||
+      !aligned(y, y_type == MOE_F32 ? 4 : 2))
+    return MOE_ERR_INVALID;
+  if (add == y && y_type != MOE_F32) return MOE_ERR_INVALID;
+  IntMatmulArgs a{};
+  a.xq = xq;
+  a.xs = x_scale;
+  a.T = T;
+  a.wq = wq;
+  a.ws = w_scale;
+  a.N = N;
+  a.K = K;
+  a.add = add;
+  a.row_w = row_w;
+  a.y = y;
+  a.y_f32 = y_type == MOE_F32;
+  a.dev_err = dev_err;
+  a.wait_limit = wait_limit_cycles();
+  return cuda_status(launch_int_matmul(a, device_sms(), stream));
 }
 
 moe_status moe_exp_portable(const float* x, int64_t n, float* out, cudaStream_t stream) {

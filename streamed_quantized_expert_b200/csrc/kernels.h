@@ -70,6 +70,53 @@ struct FfnArgs {
 // experts a layer may have for the fused decode kernel to route its token itself
 constexpr int kRouteMaxExperts = 1024;
 
+// moe_route_grouped
+struct RouteGroupedArgs {
+  const float* logits;
+  int T, E, k;
+  int G, top, gtop;  // groups, groups kept, experts that make a group's score
+  int sigmoid, renorm;
+  float scale;
+  const float* bias;
+  float L;
+  const int32_t* table;
+  int ns;
+  const float* shared_w;
+  int32_t* ids;
+  float* w;
+};
+constexpr int kRouteMaxGroups = 32;
+
+// moe_quantize_channels, moe_add_norm_quant, moe_swiglu_quant
+enum { kRowPlain = 0, kRowNorm = 1, kRowSwiglu = 2 };
+struct RowQuantArgs {
+  const void* in;         // [T][H], or [T][2H] (SwiGLU: gate columns, then up columns)
+  const void* delta;      // norm: [T][H] or null
+  const uint16_t* gamma;  // norm: [H]
+  float eps;
+  int H;  // columns of a quantised row
+  void* h_out;
+  uint16_t* x;
+  int8_t* q;
+  float* scale;
+};
+
+// moe_int_matmul
+struct IntMatmulArgs {
+  const int8_t* xq;
+  const float* xs;
+  int T;
+  const int8_t* wq;
+  const float* ws;
+  int N, K;
+  const float* add;
+  const float* row_w;
+  void* y;
+  int y_f32;
+  int32_t* dev_err;
+  long long wait_limit;
+};
+
 // Launch with programmatic stream serialization, so the kernel's CTAs can be
 // scheduled while the previous kernel in the stream drains; every kernel
 // calls griddepcontrol.wait before reading what earlier kernels wrote.
@@ -110,6 +157,9 @@ cudaError_t launch_exp(const float* x, int64_t n, float* out, cudaStream_t st);
 cudaError_t launch_quantize(const float* w, int rows, int K, int g, int b, int gu_I, uint8_t* q, cudaStream_t st);
 cudaError_t launch_dequant_slot(const uint8_t* slot, const moe_layer_desc& d, const Layout& L, float* out32,
                                 uint16_t* out16, cudaStream_t st);
+cudaError_t launch_route_grouped(const RouteGroupedArgs& a, cudaStream_t st);
+cudaError_t launch_row_quant(const RowQuantArgs& a, int op, bool in_f32, bool delta_f32, int T, cudaStream_t st);
+cudaError_t launch_int_matmul(const IntMatmulArgs& a, int num_sms, cudaStream_t st);
 bool ffn_decode_supported(const moe_layer_desc& d);
 cudaError_t launch_ffn_decode(FfnArgs a, const moe_layer_desc& d, int num_sms, cudaStream_t st);
 cudaError_t launch_ffn_route_fused(FfnArgs a, const moe_layer_desc& d, int num_sms, cudaStream_t st);

@@ -16,6 +16,8 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 MOE_OK, MOE_ERR_INVALID, MOE_ERR_CUDA, MOE_ERR_UNSUPPORTED, MOE_ERR_NOT_RESIDENT, MOE_ERR_CAPACITY, \
     MOE_ERR_TIMEOUT = range(7)
 DEV_ERR_NOT_RESIDENT, DEV_ERR_SLOT_RANGE, DEV_ERR_TIMEOUT, DEV_ERR_BAD_EXPERT = 1, 2, 4, 8
+MOE_BF16, MOE_F32 = 0, 1  # element types
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 WS_CONTROL_BYTES = 512  # head of the workspace: the control block (include/moe.h, moe_workspace_bytes)
 
 # every entry point declared in include/moe.h
@@ -28,6 +30,7 @@ ABI_SYMBOLS = [
     "moe_last_cuda_error", "moe_ffn_kernel_path", "moe_set_wait_limit_cycles", "moe_route_shared",
     "moe_router_logits", "moe_cache_reserve", "moe_cache_commit", "moe_prefetch_create", "moe_prefetch_destroy",
     "moe_prefetch_stats", "moe_decode_layer_ahead", "moe_route_sort_lookup", "moe_route_expert_ffn",
+    "moe_route_grouped", "moe_add_norm_quant", "moe_quantize_channels", "moe_swiglu_quant", "moe_int_matmul",
 ]
 
 
@@ -68,6 +71,16 @@ class GuessBuffers(C.Structure):
     _fields_ = [("ids", C.c_void_p), ("w", C.c_void_p), ("ids_host", C.c_void_p), ("stride", C.c_int32)]
 
 
+class RouteConfig(C.Structure):
+    """How moe_route_grouped scores and chooses (moe_route_config)."""
+    _fields_ = [("score", C.c_int32), ("n_groups", C.c_int32), ("top_groups", C.c_int32), ("group_top", C.c_int32),
+                ("renormalise", C.c_int32), ("scale", C.c_float)]
+
+    def __repr__(self):
+        return (f"RouteConfig(score={self.score}, n_groups={self.n_groups}, top_groups={self.top_groups}, "
+                f"group_top={self.group_top}, renormalise={self.renormalise}, scale={self.scale})")
+
+
 class SlotLayout(C.Structure):
     _fields_ = [("gate_up", C.c_uint64), ("down", C.c_uint64), ("gate_up_tile_bytes", C.c_uint64),
                 ("down_tile_bytes", C.c_uint64), ("slot_bytes", C.c_uint64)]
@@ -101,6 +114,11 @@ def lib():
             "moe_noalloc_scratch_bytes": (sz, []),
             "moe_dequant_slot": (C.c_int, [P, i32, D, P, P, P]),
             "moe_quantize_rows": (C.c_int, [P, i32, i32, i32, i32, i32, P, P]),
+            "moe_route_grouped": (C.c_int, [P, i32, D, C.POINTER(RouteConfig), P, f32, P, i32, P, P, P, P]),
+            "moe_add_norm_quant": (C.c_int, [P, i32, P, i32, P, f32, i32, i32, P, P, P, P, P]),
+            "moe_quantize_channels": (C.c_int, [P, i32, i32, i32, P, P, P]),
+            "moe_swiglu_quant": (C.c_int, [P, i32, i32, i32, P, P, P]),
+            "moe_int_matmul": (C.c_int, [P, P, i32, P, P, i32, i32, P, P, P, i32, P, P]),
             "moe_exp_portable": (C.c_int, [P, i64, P, P]),
             "moe_status_string": (C.c_char_p, [C.c_int]),
             "moe_last_cuda_error": (C.c_char_p, []),
@@ -295,6 +313,48 @@ def moe_quantize_rows(w, rows, K, group, bits, proj, stream=None, gate_up_I=0) -
 
 def moe_exp_portable(x, n, out, stream=None) -> None:
     _ck(lib().moe_exp_portable(_ptr(x), int(n), _ptr(out), _stream(stream)), "moe_exp_portable")
+
+
+# ---------------------------------------------------------------------------
+# operators around the routed experts
+# ---------------------------------------------------------------------------
+def route_config(score="softmax", n_groups=1, top_groups=1, group_top=1, renormalise=True, scale=1.0) -> RouteConfig:
+    """score: "softmax", "sigmoid" or a MOE_SCORE_* value."""
+    sc = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}.get(score, score)
+    return RouteConfig(int(sc), int(n_groups), int(top_groups), int(group_top), 1 if renormalise else 0, float(scale))
+
+
+def moe_route_grouped(logits, T, d, config: RouteConfig, bias, L, slot_table, n_shared, shared_w, ids, w,
+                      stream=None) -> None:
+    """Top-k by softmax or sigmoid scores with a bias and groups; outputs as moe_route_shared."""
+    _ck(lib().moe_route_grouped(_ptr(logits), int(T), C.byref(d), None if config is None else C.byref(config),
+                                _ptr(bias), float(L), _ptr(slot_table), int(n_shared), _ptr(shared_w), _ptr(ids),
+                                _ptr(w), _stream(stream)), "moe_route_grouped")
+
+
+def moe_add_norm_quant(h, h_type, delta, delta_type, gamma, eps, T, H, h_out, x, q, q_scale, stream=None) -> None:
+    """Residual sum, RMS norm (bf16 x) and the norm's 8-bit codes with a scale per row."""
+    _ck(lib().moe_add_norm_quant(_ptr(h), int(h_type), _ptr(delta), int(delta_type), _ptr(gamma), float(eps), int(T),
+                                 int(H), _ptr(h_out), _ptr(x), _ptr(q), _ptr(q_scale), _stream(stream)),
+        "moe_add_norm_quant")
+
+
+def moe_quantize_channels(w, w_type, rows, K, q, scale, stream=None) -> None:
+    """8-bit codes of plain rows, one scale per row."""
+    _ck(lib().moe_quantize_channels(_ptr(w), int(w_type), int(rows), int(K), _ptr(q), _ptr(scale), _stream(stream)),
+        "moe_quantize_channels")
+
+
+def moe_swiglu_quant(gu, gu_type, T, I, q, q_scale, stream=None) -> None:
+    """silu(gate) * up of rows [gate | up], as 8-bit codes with a scale per row."""
+    _ck(lib().moe_swiglu_quant(_ptr(gu), int(gu_type), int(T), int(I), _ptr(q), _ptr(q_scale), _stream(stream)),
+        "moe_swiglu_quant")
+
+
+def moe_int_matmul(xq, x_scale, T, wq, w_scale, N, K, add, row_w, y, y_type, dev_err, stream=None) -> None:
+    """y = add + row_w x_scale w_scale (xq . wq^T), int32 accumulation."""
+    _ck(lib().moe_int_matmul(_ptr(xq), _ptr(x_scale), int(T), _ptr(wq), _ptr(w_scale), int(N), int(K), _ptr(add),
+                             _ptr(row_w), _ptr(y), int(y_type), _ptr(dev_err), _stream(stream)), "moe_int_matmul")
 
 
 # ---------------------------------------------------------------------------
