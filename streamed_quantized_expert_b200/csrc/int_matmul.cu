@@ -1,71 +1,401 @@
 // Product of 8-bit integer rows with a scale per token and per output
 // (moe_int_matmul): y[t][n] = add[t][n] + row_w[t] xs[t] ws[n] sum_k xq[t][k] wq[n][k].
 //
-// The sum is a whole number below 2^31 (K <= 65,536), so int32 accumulation
-// is exact in any order; the scales are applied once to each sum.
+// The sum is a whole number of at most 2^30 (K <= 65,536), so int32
+// accumulation is exact in any order and any split of K gives the same bits;
+// the scales are applied once to each sum.
+//
+// Up to 16 tokens the weight bytes bound the call: im_rows_kernel streams
+// them through mma.sync, one block per 16 outputs.  Above, im_tc_kernel runs
+// on tcgen05 (kind::i8, s32 accumulators in TMEM) fed by TMA, with the weight
+// rows as the MMA's 128-row side so that a few dozen tokens fill its other side.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
 #include "common.cuh"
+#include "ffn_common.cuh"
 #include "kernels.h"
 
 namespace moe {
 namespace {
 
-constexpr int kTile = 64, kKc = 64;  // outputs and tokens of a block; inputs of a step
+__device__ __forceinline__ float im_scaled(int acc, float xs, float ws) { return (float)acc * (xs * ws); }
 
-__global__ void __launch_bounds__(256) int_matmul_kernel(const IntMatmulArgs a) {
-  __shared__ int s_w[kTile][kKc / 4 + 1], s_x[kTile][kKc / 4 + 1];
+__device__ __forceinline__ float im_token_scale(const IntMatmulArgs& a, int t) {
+  return a.row_w ? a.xs[t] * a.row_w[t] : a.xs[t];
+}
+
+__device__ __forceinline__ void im_store(const IntMatmulArgs& a, int t, int n, float v) {
+  const int64_t at = (int64_t)t * a.N + n;
+  if (a.add) v += a.add[at];
+  if (a.y_f32)
+    static_cast<float*>(a.y)[at] = v;
+  else
+    static_cast<uint16_t*>(a.y)[at] = f32_to_bf16_rne(v);
+}
+
+// ---------------------------------------------------------------------------
+// few tokens
+// ---------------------------------------------------------------------------
+constexpr int kRowsTokens = 16;  // tokens the streaming kernel takes
+constexpr int kRowsWarps = 8;    // warps of a block, taking turns along K
+constexpr int kRowsUnroll = 4;   // 64-input blocks a warp loads at a time
+
+// D (16 x 8, s32) += A (16 x 32, s8, row) . B (32 x 8, s8, column).
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 ld_stream(const int8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// One block: 16 outputs, up to 8 NT tokens, the whole of K.  A warp takes
+// 64-input blocks in turn; lane (g, q) loads the 16 bytes q of rows g and
+// g + 8 and of token g, which are the fragments of two MMAs over inputs that
+// both operands permute alike: bytes 16 q + 0..7 of every lane are the first
+// MMA's inputs, 16 q + 8..15 the second's.  The warps' sums meet in shared memory.
+template <int NT>
+__global__ void __launch_bounds__(32 * kRowsWarps) im_rows_kernel(const IntMatmulArgs a) {
+  __shared__ int s_acc[kRowsWarps][NT][4][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+  const int n0 = blockIdx.x * 16;
   pdl_wait();
   pdl_launch_dependents();
-  const int n0 = blockIdx.x * kTile, t0 = blockIdx.y * kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  int acc[4][4] = {};
-  for (int k0 = 0; k0 < a.K; k0 += kKc) {
-    for (int i = threadIdx.x; i < kTile * (kKc / 4); i += 256) {
-      const int r = i / (kKc / 4), c = i % (kKc / 4), k = k0 + 4 * c;
-      const bool in = k < a.K;
-      s_w[r][c] = in && n0 + r < a.N ? *reinterpret_cast<const int*>(a.wq + (int64_t)(n0 + r) * a.K + k) : 0;
-      s_x[r][c] = in && t0 + r < a.T ? *reinterpret_cast<const int*>(a.xq + (int64_t)(t0 + r) * a.K + k) : 0;
+  const int8_t* wa = n0 + g < a.N ? a.wq + (int64_t)(n0 + g) * a.K : nullptr;
+  const int8_t* wb = n0 + g + 8 < a.N ? a.wq + (int64_t)(n0 + g + 8) * a.K : nullptr;
+  int acc[NT][4] = {};
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  for (int k0 = 64 * warp; k0 < a.K; k0 += 64 * kRowsWarps * kRowsUnroll) {
+    uint4 va[kRowsUnroll], vb[kRowsUnroll];
+#pragma unroll
+    for (int u = 0; u < kRowsUnroll; ++u) {
+      const int k = k0 + 64 * kRowsWarps * u + 16 * q;  // K is a multiple of 16
+      va[u] = wa && k < a.K ? ld_stream(wa + k) : zero;
+      vb[u] = wb && k < a.K ? ld_stream(wb + k) : zero;
     }
-    __syncthreads();
 #pragma unroll
-    for (int c = 0; c < kKc / 4; ++c)
+    for (int u = 0; u < kRowsUnroll; ++u) {
+      const int k = k0 + 64 * kRowsWarps * u + 16 * q;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(s_x[ty + 16 * i][c], s_w[tx + 16 * j][c], acc[i][j]);
-    __syncthreads();
+      for (int j = 0; j < NT; ++j) {
+        const int t = 8 * j + g;
+        const uint4 x = t < a.T && k < a.K ? *reinterpret_cast<const uint4*>(a.xq + (int64_t)t * a.K + k) : zero;
+        mma_s8(acc[j], va[u].x, vb[u].x, va[u].y, vb[u].y, x.x, x.y);
+        mma_s8(acc[j], va[u].z, vb[u].z, va[u].w, vb[u].w, x.z, x.w);
+      }
+    }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int t = t0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (t >= a.T || n >= a.N) continue;
-      const int64_t at = (int64_t)t * a.N + n;
-      const float xs = a.row_w ? a.xs[t] * a.row_w[t] : a.xs[t];
-      float v = (float)acc[i][j] * (xs * a.ws[n]);
-      if (a.add) v += a.add[at];
-      if (a.y_f32)
-        static_cast<float*>(a.y)[at] = v;
-      else
-        static_cast<uint16_t*>(a.y)[at] = f32_to_bf16_rne(v);
+    for (int i = 0; i < 4; ++i) s_acc[warp][j][i][lane] = acc[j][i];
+  __syncthreads();
+  // accumulator i of lane (g, q): output g + 8 (i / 2), token 2 q + i % 2
+  for (int o = threadIdx.x; o < NT * 128; o += 32 * kRowsWarps) {
+    const int n = o & 15, t = o >> 4, j = t >> 3, i = 2 * (n >> 3) + (t & 1), l = 4 * (n & 7) + ((t & 7) >> 1);
+    if (n0 + n >= a.N || t >= a.T) continue;
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < kRowsWarps; ++w) sum += s_acc[w][j][i][l];
+    im_store(a, t, n0 + n, im_scaled(sum, im_token_scale(a, t), a.ws[n0 + n]));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// many tokens
+// ---------------------------------------------------------------------------
+constexpr int kTcBM = 128;  // outputs of a tile (MMA M)
+constexpr int kTcBK = 128;  // inputs of a stage: one 128-byte swizzled row per output and token
+constexpr int kTcProdWarp = 0, kTcMmaWarp = 1, kTcEpiWarp0 = 4, kTcEpiWarps = 8;
+constexpr int kTcThreads = 32 * (kTcEpiWarp0 + kTcEpiWarps);
+__host__ __device__ constexpr int tc_stages(int nb) { return nb == 256 ? 4 : nb == 128 ? 6 : 8; }
+__host__ __device__ constexpr int tc_stage_bytes(int nb) { return (kTcBM + nb) * kTcBK; }
+__host__ __device__ constexpr int tc_smem_bytes(int nb) { return tc_stages(nb) * tc_stage_bytes(nb) + 1024 + 256; }
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* tm, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_addr(dst)),
+      "l"(tm), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tmap_prefetch(const CUtensorMap* tm) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(tm) : "memory");
+}
+// Descriptor of a K-major operand of 128-byte swizzled rows, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1u << 16) | ((uint64_t)(1024u >> 4) << 32) |
+         ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+// Instruction descriptor, kind::i8: s32 accumulator (bits 4-5 = 2), A and B
+// signed (bits 7-9 = 1, bits 10-12 = 1), both K-major, N >> 3 in bits 17-22, M >> 4 in bits 24-28.
+__device__ __forceinline__ uint32_t idesc_s8(int M, int N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// D (TMEM, s32) (+)= A . B^T over 32 inputs, both operands in shared memory.
+__device__ __forceinline__ void umma_s8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// 32 TMEM lanes x 32 columns: thread i gets lane (base lane + i).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Bounded wait that also gives up once another role of the CTA has aborted.
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                        long long limit_cycles) {
+  if (mbar_test(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    if (mbar_try_wait(bar, parity, 20000u)) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > limit_cycles) {
+      *abort_flag = 1;
+      return false;
     }
+  }
+}
+
+// Persistent: CTA i takes tiles i, i + grid, ... of 128 outputs x NB tokens
+// (the outputs' tiles fastest).  Warp 0 loads stages by TMA, warp 1 issues
+// the MMAs, warps 4-11 scale and store; accumulators are double-buffered in
+// TMEM, so that a tile's stores run under the next one's MMAs.  Inputs past K
+// and rows past N or T arrive as zeros.
+template <int NB>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    im_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                 const IntMatmulArgs a, const int mtiles, const int ntiles) {
+  extern __shared__ uint8_t im_smem[];
+  constexpr int kStages = tc_stages(NB), kStage = tc_stage_bytes(NB), kCols = 2 * NB;
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(im_smem) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(base + kStages * kStage);  // TMA -> MMA
+  uint64_t* empty = full + kStages;                                       // MMA -> TMA
+  uint64_t* accfull = empty + kStages;                                    // MMA -> epilogue
+  uint64_t* accempty = accfull + 2;                                       // epilogue -> MMA
+  uint64_t* drain = accempty + 2;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  __shared__ float s_xs[kTcEpiWarps][32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int c = 0; c < 2; ++c) {
+      mbar_init(&accfull[c], 1);
+      mbar_init(&accempty[c], kTcEpiWarps);
+    }
+    mbar_init(drain, 1);
+    fence_barrier_init();
+    s_abort = 0;
+    tmap_prefetch(&tm_w);
+    tmap_prefetch(&tm_x);
+  }
+  if (warp == kTcMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem)),
+                 "r"(kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const int nkb = (a.K + kTcBK - 1) / kTcBK, tiles = mtiles * ntiles;
+  pdl_wait();
+
+  if (warp == kTcProdWarp) {
+    if (lane == 0) {
+      asm volatile("fence.proxy.async.global;" ::: "memory");  // rows that earlier kernels wrote, to TMA's reads
+      int s = 0;
+      uint32_t ph = 0, issued = 0, last_ph = 0;
+      for (int t = blockIdx.x; t < tiles && !s_abort; t += gridDim.x) {
+        const int m0 = (t % mtiles) * kTcBM, t0 = (t / mtiles) * NB;
+        bool ok = true;
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!tc_wait(&empty[s], ph ^ 1u, &s_abort, a.wait_limit)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = base + s * kStage;
+          mbar_arrive_expect_tx(&full[s], kStage);
+          tma_load_2d(st, &tm_w, kb * kTcBK, m0, &full[s]);
+          tma_load_2d(st + kTcBM * kTcBK, &tm_x, kb * kTcBK, t0, &full[s]);
+          issued |= 1u << s;
+          last_ph = (last_ph & ~(1u << s)) | (ph << s);
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+      }
+      for (int q = 0; q < kStages; ++q)  // every copy issued lands before the CTA can exit
+        if ((issued >> q) & 1u) mbar_wait_bounded(&full[q], (last_ph >> q) & 1u, a.wait_limit);
+    }
+  } else if (warp == kTcMmaWarp) {
+    if (lane == 0) {
+      int s = 0, c = 0;
+      uint32_t ph = 0, pc = 0;
+      bool issued_any = false;
+      for (int t = blockIdx.x; t < tiles && !s_abort; t += gridDim.x) {
+        const int t0 = (t / mtiles) * NB, n = a.T - t0 < NB ? a.T - t0 : NB;
+        const uint32_t idesc = idesc_s8(kTcBM, (n + 31) & ~31);
+        if (!tc_wait(&accempty[c], pc ^ 1u, &s_abort, a.wait_limit)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(c * NB);
+        bool ok = true;
+        for (int kb = 0; kb < nkb; ++kb) {
+          const uint64_t ad = sw128_desc(smem_addr(base + s * kStage));
+          const uint64_t bd = sw128_desc(smem_addr(base + s * kStage + kTcBM * kTcBK));
+          if (!tc_wait(&full[s], ph, &s_abort, a.wait_limit)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < kTcBK / 32; ++k) umma_s8(d, ad + 2 * k, bd + 2 * k, idesc, (kb | k) != 0 ? 1u : 0u);
+          issued_any = true;
+          umma_commit(&empty[s]);
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit(&accfull[c]);
+        if (++c == 2) {
+          c = 0;
+          pc ^= 1u;
+        }
+      }
+      if (issued_any) {  // every MMA issued completes before TMEM is freed
+        umma_commit(drain);
+        mbar_wait_bounded(drain, 0, a.wait_limit);
+      }
+    }
+  } else if (warp >= kTcEpiWarp0) {
+    // warp i reads TMEM lanes 32 (i % 4)..; the two warps of a quadrant take alternate 32-token chunks
+    const int q = warp & 3, half = (warp - kTcEpiWarp0) >> 2;
+    float* xs = s_xs[warp - kTcEpiWarp0];
+    int c = 0;
+    uint32_t pc = 0;
+    for (int t = blockIdx.x; t < tiles && !s_abort; t += gridDim.x) {
+      const int n = (t % mtiles) * kTcBM + 32 * q + lane, t0 = (t / mtiles) * NB;
+      const float ws = n < a.N ? a.ws[n] : 0.0f;
+      if (!tc_wait(&accfull[c], pc, &s_abort, a.wait_limit)) break;
+      tc_fence_after();
+      for (int col = 32 * half; col < NB && t0 + col < a.T; col += 64) {
+        uint32_t v[32];
+        __syncwarp();
+        xs[lane] = t0 + col + lane < a.T ? im_token_scale(a, t0 + col + lane) : 0.0f;
+        __syncwarp();
+        tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(c * NB + col), v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (n < a.N && t0 + col + i < a.T) im_store(a, t0 + col + i, n, im_scaled((int)v[i], xs[i], ws));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&accempty[c]);
+      if (++c == 2) {
+        c = 0;
+        pc ^= 1u;
+      }
+    }
+  }
+  pdl_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (s_abort && tid == 0 && a.dev_err) atomicOr(a.dev_err, MOE_DEV_ERR_TIMEOUT);
+  if (warp == kTcMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// Rows of K bytes; a box is `rows` rows x 128 bytes, 128-byte swizzled.
+bool encode_rows(CUtensorMap* m, const int8_t* p, int n, int K, int rows) {
+  const auto fn = tmap_encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)n}, strides[1] = {(cuuint64_t)K};
+  const cuuint32_t box[2] = {(cuuint32_t)kTcBK, (cuuint32_t)rows}, es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(p), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NB>
+cudaError_t launch_tc(const IntMatmulArgs& a, int num_sms, cudaStream_t st) {
+  static int smem_set[4] = {0, 0, 0, 0};
+  const void* kern = reinterpret_cast<const void*>(im_tc_kernel<NB>);
+  cudaError_t e = ensure_smem_attr(kern, smem_set);
+  if (e != cudaSuccess) return e;
+  CUtensorMap tw, tx;
+  if (!encode_rows(&tw, a.wq, a.N, a.K, kTcBM) || !encode_rows(&tx, a.xq, a.T, a.K, NB)) return cudaErrorInvalidValue;
+  const int mtiles = (a.N + kTcBM - 1) / kTcBM, ntiles = (a.T + NB - 1) / NB;
+  const int64_t tiles = (int64_t)mtiles * ntiles;
+  return launch_pdl(kern, (int)(tiles < num_sms ? tiles : num_sms), kTcThreads, tc_smem_bytes(NB), st, tw, tx, a,
+                    mtiles, ntiles);
 }
 
 }  // namespace
 
 cudaError_t launch_int_matmul(const IntMatmulArgs& a, int num_sms, cudaStream_t st) {
-  (void)num_sms;
-  const dim3 grid((unsigned)((a.N + kTile - 1) / kTile), (unsigned)((a.T + kTile - 1) / kTile));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, int_matmul_kernel, a);
+  if (a.T <= kRowsTokens) {
+    const void* kern = a.T <= 8 ? reinterpret_cast<const void*>(im_rows_kernel<1>)
+                                : reinterpret_cast<const void*>(im_rows_kernel<2>);
+    return launch_pdl(kern, (a.N + 15) / 16, 32 * kRowsWarps, 0, st, a);
+  }
+  if (a.T <= 32) return launch_tc<32>(a, num_sms, st);
+  if (a.T <= 64) return launch_tc<64>(a, num_sms, st);
+  if (a.T <= 128) return launch_tc<128>(a, num_sms, st);
+  return launch_tc<256>(a, num_sms, st);
 }
 
 }  // namespace moe
