@@ -40,8 +40,8 @@ __device__ __forceinline__ void im_store(const IntMatmulArgs& a, int t, int n, f
 // few tokens
 // ---------------------------------------------------------------------------
 constexpr int kRowsTokens = 16;  // tokens the streaming kernel takes
-constexpr int kRowsWarps = 8;    // warps of a block, taking turns along K
-constexpr int kRowsUnroll = 4;   // 64-input blocks a warp loads at a time
+// 128-input units a warp keeps in flight; the registers hold fewer next to two token tiles
+__host__ __device__ constexpr int rows_depth(int nt) { return nt == 1 ? 4 : 2; }
 
 // D (16 x 8, s32) += A (16 x 32, s8, row) . B (32 x 8, s8, column).
 __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -59,40 +59,58 @@ __device__ __forceinline__ uint4 ld_stream(const int8_t* p) {
   return v;
 }
 
-// One block: 16 outputs, up to 8 NT tokens, the whole of K.  A warp takes
-// 64-input blocks in turn; lane (g, q) loads the 16 bytes q of rows g and
-// g + 8 and of token g, which are the fragments of two MMAs over inputs that
-// both operands permute alike: bytes 16 q + 0..7 of every lane are the first
-// MMA's inputs, 16 q + 8..15 the second's.  The warps' sums meet in shared memory.
-template <int NT>
-__global__ void __launch_bounds__(32 * kRowsWarps) im_rows_kernel(const IntMatmulArgs a) {
-  __shared__ int s_acc[kRowsWarps][NT][4][32];
+// One block: 16 outputs, up to 8 NT tokens, the whole of K, its W warps taking
+// units of 128 inputs in turn.  Lane (g, q) loads bytes 16 q and 64 + 16 q of
+// the unit's rows g and g + 8 and of token g (whole 128-byte lines per row);
+// they are the fragments of four MMAs over inputs that both operands permute
+// alike: bytes 0..7 of the lanes' 16 are one MMA's inputs, 8..15 the next one's.
+// A ring of rows_depth units in registers keeps 2 KB a unit and warp on the
+// way (128 KB an SM at two blocks of eight warps: what 6.5 TB/s needs at HBM
+// latency).  Rows past N and tokens past T read the last one's and are not
+// stored.  The warps' sums meet in shared memory.
+template <int NT, int W>
+__global__ void __launch_bounds__(32 * W, 16 / W) im_rows_kernel(const IntMatmulArgs a) {
+  constexpr int kDepth = rows_depth(NT);
+  __shared__ int s_acc[W][NT][4][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-  const int n0 = blockIdx.x * 16;
+  const int n0 = blockIdx.x * 16, U = (a.K + 127) / 128;
+  const int8_t* wa = a.wq + (int64_t)min(n0 + g, a.N - 1) * a.K + 16 * q;
+  const int8_t* wb = a.wq + (int64_t)min(n0 + g + 8, a.N - 1) * a.K + 16 * q;
+  const int8_t* xp[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) xp[j] = a.xq + (int64_t)min(8 * j + g, a.T - 1) * a.K + 16 * q;
   pdl_wait();
   pdl_launch_dependents();
-  const int8_t* wa = n0 + g < a.N ? a.wq + (int64_t)(n0 + g) * a.K : nullptr;
-  const int8_t* wb = n0 + g + 8 < a.N ? a.wq + (int64_t)(n0 + g + 8) * a.K : nullptr;
   int acc[NT][4] = {};
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  for (int k0 = 64 * warp; k0 < a.K; k0 += 64 * kRowsWarps * kRowsUnroll) {
-    uint4 va[kRowsUnroll], vb[kRowsUnroll];
+  uint4 w[kDepth][4], x[kDepth][NT][2];
+  auto load = [&](int u, uint4 (&wv)[4], uint4 (&xv)[NT][2]) {
 #pragma unroll
-    for (int u = 0; u < kRowsUnroll; ++u) {
-      const int k = k0 + 64 * kRowsWarps * u + 16 * q;  // K is a multiple of 16
-      va[u] = wa && k < a.K ? ld_stream(wa + k) : zero;
-      vb[u] = wb && k < a.K ? ld_stream(wb + k) : zero;
+    for (int h = 0; h < 2; ++h) {
+      const int k = 128 * u + 64 * h;  // this lane's 16 inputs: k + 16 q ..; K is a multiple of 16
+      const bool in = u < U && k + 16 * q < a.K;
+      wv[2 * h] = in ? ld_stream(wa + k) : make_uint4(0u, 0u, 0u, 0u);
+      wv[2 * h + 1] = in ? ld_stream(wb + k) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        if (in) xv[j][h] = *reinterpret_cast<const uint4*>(xp[j] + k);  // else any value: its weights are 0
     }
+  };
 #pragma unroll
-    for (int u = 0; u < kRowsUnroll; ++u) {
-      const int k = k0 + 64 * kRowsWarps * u + 16 * q;
+  for (int i = 0; i < kDepth; ++i) load(warp + i * W, w[i], x[i]);
+  for (int u0 = warp; u0 < U; u0 += kDepth * W) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int t = 8 * j + g;
-        const uint4 x = t < a.T && k < a.K ? *reinterpret_cast<const uint4*>(a.xq + (int64_t)t * a.K + k) : zero;
-        mma_s8(acc[j], va[u].x, vb[u].x, va[u].y, vb[u].y, x.x, x.y);
-        mma_s8(acc[j], va[u].z, vb[u].z, va[u].w, vb[u].w, x.z, x.w);
+    for (int i = 0; i < kDepth; ++i) {
+      if (u0 + i * W >= U) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 va = w[i][2 * h], vb = w[i][2 * h + 1];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          mma_s8(acc[j], va.x, vb.x, va.y, vb.y, x[i][j][h].x, x[i][j][h].y);
+          mma_s8(acc[j], va.z, vb.z, va.w, vb.w, x[i][j][h].z, x[i][j][h].w);
+        }
       }
+      load(u0 + (kDepth + i) * W, w[i], x[i]);
     }
   }
 #pragma unroll
@@ -101,12 +119,12 @@ __global__ void __launch_bounds__(32 * kRowsWarps) im_rows_kernel(const IntMatmu
     for (int i = 0; i < 4; ++i) s_acc[warp][j][i][lane] = acc[j][i];
   __syncthreads();
   // accumulator i of lane (g, q): output g + 8 (i / 2), token 2 q + i % 2
-  for (int o = threadIdx.x; o < NT * 128; o += 32 * kRowsWarps) {
+  for (int o = threadIdx.x; o < NT * 128; o += 32 * W) {
     const int n = o & 15, t = o >> 4, j = t >> 3, i = 2 * (n >> 3) + (t & 1), l = 4 * (n & 7) + ((t & 7) >> 1);
     if (n0 + n >= a.N || t >= a.T) continue;
     int sum = 0;
 #pragma unroll
-    for (int w = 0; w < kRowsWarps; ++w) sum += s_acc[w][j][i][l];
+    for (int v = 0; v < W; ++v) sum += s_acc[v][j][i][l];
     im_store(a, t, n0 + n, im_scaled(sum, im_token_scale(a, t), a.ws[n0 + n]));
   }
 }
@@ -384,13 +402,20 @@ cudaError_t launch_tc(const IntMatmulArgs& a, int num_sms, cudaStream_t st) {
                     mtiles, ntiles);
 }
 
+template <int NT>
+const void* rows_kernel(int W) {
+  return W == 8   ? reinterpret_cast<const void*>(im_rows_kernel<NT, 8>)
+         : W == 4 ? reinterpret_cast<const void*>(im_rows_kernel<NT, 4>)
+                  : reinterpret_cast<const void*>(im_rows_kernel<NT, 2>);
+}
+
 }  // namespace
 
 cudaError_t launch_int_matmul(const IntMatmulArgs& a, int num_sms, cudaStream_t st) {
   if (a.T <= kRowsTokens) {
-    const void* kern = a.T <= 8 ? reinterpret_cast<const void*>(im_rows_kernel<1>)
-                                : reinterpret_cast<const void*>(im_rows_kernel<2>);
-    return launch_pdl(kern, (a.N + 15) / 16, 32 * kRowsWarps, 0, st, a);
+    // enough units for each warp to fill its ring
+    const int W = a.K >= 4096 ? 8 : a.K >= 2048 ? 4 : 2;
+    return launch_pdl(a.T <= 8 ? rows_kernel<1>(W) : rows_kernel<2>(W), (a.N + 15) / 16, 32 * W, 0, st, a);
   }
   if (a.T <= 32) return launch_tc<32>(a, num_sms, st);
   if (a.T <= 64) return launch_tc<64>(a, num_sms, st);
