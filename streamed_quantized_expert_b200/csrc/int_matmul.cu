@@ -10,8 +10,10 @@
 // on tcgen05 (kind::i8, s32 accumulators in TMEM) fed by TMA, with the weight
 // rows as the MMA's 128-row side so that a few dozen tokens fill its other side.
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "common.cuh"
@@ -135,6 +137,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) im_rows_kernel(const IntMatmul
 constexpr int kTcBM = 128;  // outputs of a tile (MMA M)
 constexpr int kTcBK = 128;  // inputs of a stage: one 128-byte swizzled row per output and token
 constexpr int kTcProdWarp = 0, kTcMmaWarp = 1, kTcEpiWarp0 = 4, kTcEpiWarps = 8;
+constexpr int kTcSplitMaxTokens = 64;  // token tiles whose K may be split
+constexpr int kTcSplitCtas = 128;      // CTAs of a split call: clusters of up to 8 that 148 SMs take at once
 constexpr int kTcThreads = 32 * (kTcEpiWarp0 + kTcEpiWarps);
 __host__ __device__ constexpr int tc_stages(int nb) { return nb == 256 ? 4 : nb == 128 ? 6 : 8; }
 __host__ __device__ constexpr int tc_stage_bytes(int nb) { return (kTcBM + nb) * kTcBK; }
@@ -203,15 +207,84 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile
   }
 }
 
-// Persistent: CTA i takes tiles i, i + grid, ... of 128 outputs x NB tokens
-// (the outputs' tiles fastest).  Warp 0 loads stages by TMA, warp 1 issues
-// the MMAs, warps 4-11 scale and store; accumulators are double-buffered in
-// TMEM, so that a tile's stores run under the next one's MMAs.  Inputs past K
-// and rows past N or T arrive as zeros.
-template <int NB>
+// 32 tokens (t.., the first `cnt` of them exist) of one output per lane, from
+// the accumulators v: y is written 128 (fp32) or 64 (bf16) contiguous bytes
+// per token and warp.  xs: the tokens' scales.  With `pairs` (N even, y
+// 4-byte aligned) two lanes swap halves, so that one of them writes both
+// outputs of the even token and the other both of the odd one.
+template <bool FULL>
+__device__ __forceinline__ void im_store_chunk(const IntMatmulArgs& a, const uint32_t (&v)[32], const float* xs,
+                                               float ws, int n, int t, int cnt, bool pairs) {
+  const bool in = n < a.N;
+  const int64_t at = (int64_t)t * a.N + n;
+#pragma unroll
+  for (int i0 = 0; i0 < 32; i0 += 8) {
+    if (!FULL && i0 >= cnt) break;
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = im_scaled((int)v[i0 + i], xs[i0 + i], ws);
+    if (a.add) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (in && (FULL || i0 + i < cnt)) f[i] += a.add[at + (int64_t)(i0 + i) * a.N];
+    }
+    if (a.y_f32) {
+      float* y = static_cast<float*>(a.y) + at + (int64_t)i0 * a.N;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (in && (FULL || i0 + i < cnt)) y[(int64_t)i * a.N] = f[i];
+    } else if (pairs) {
+      const bool odd = n & 1;
+      uint16_t* y = static_cast<uint16_t*>(a.y) + at + (int64_t)(i0 + odd) * a.N - odd;
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? f[i] : f[i + 1], 1);
+        const __nv_bfloat162 w = odd ? __floats2bfloat162_rn(got, f[i + 1]) : __floats2bfloat162_rn(f[i], got);
+        if (in && (FULL || i0 + i + odd < cnt)) *reinterpret_cast<__nv_bfloat162*>(y + (int64_t)i * a.N) = w;
+      }
+    } else {
+      uint16_t* y = static_cast<uint16_t*>(a.y) + at + (int64_t)i0 * a.N;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (in && (FULL || i0 + i < cnt)) y[(int64_t)i * a.N] = __bfloat16_as_ushort(__float2bfloat16_rn(f[i]));
+    }
+  }
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// 16 bytes of shared memory of CTA `rank` of the cluster, at this CTA's address `saddr`.
+__device__ __forceinline__ int4 ld_cluster(uint32_t saddr, uint32_t rank) {
+  uint32_t ra;
+  int4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(saddr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(ra)
+               : "memory");
+  return v;
+}
+
+// Tiles of 128 outputs x NB tokens (the outputs' tiles fastest).  Warp 0
+// loads stages by TMA, warp 1 issues the MMAs, warps 4-11 scale and store.
+// Inputs past K and rows past N or T arrive as zeros.
+//   SPLIT false: persistent, CTA i takes tiles i, i + grid, ...; accumulators
+//     are double-buffered in TMEM, so that a tile's stores run under the next
+//     one's MMAs.
+//   SPLIT true: one tile per cluster of `split` CTAs, each with its share of
+//     K; their s32 sums meet in shared memory (the stages' space, free by
+//     then), and each CTA finishes every split-th token.
+template <int NB, bool SPLIT>
 __global__ void __launch_bounds__(kTcThreads, 1)
     im_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
-                 const IntMatmulArgs a, const int mtiles, const int ntiles) {
+                 const IntMatmulArgs a, const int mtiles, const int ntiles, const int split) {
   extern __shared__ uint8_t im_smem[];
   constexpr int kStages = tc_stages(NB), kStage = tc_stage_bytes(NB), kCols = 2 * NB;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(im_smem) + 1023) & ~uintptr_t(1023));
@@ -250,6 +323,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   const int nkb = (a.K + kTcBK - 1) / kTcBK, tiles = mtiles * ntiles;
+  const int rank = SPLIT ? (int)cluster_rank() : 0;
+  const int kb0 = SPLIT ? nkb * rank / split : 0, kb1 = SPLIT ? nkb * (rank + 1) / split : nkb;
+  const int tile0 = SPLIT ? blockIdx.x / split : blockIdx.x, step = SPLIT ? tiles : gridDim.x;
+  const bool pairs = !(a.N & 1) && !(reinterpret_cast<uintptr_t>(a.y) & 3);
   pdl_wait();
 
   if (warp == kTcProdWarp) {
@@ -257,10 +334,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       asm volatile("fence.proxy.async.global;" ::: "memory");  // rows that earlier kernels wrote, to TMA's reads
       int s = 0;
       uint32_t ph = 0, issued = 0, last_ph = 0;
-      for (int t = blockIdx.x; t < tiles && !s_abort; t += gridDim.x) {
+      for (int t = tile0; t < tiles && !s_abort; t += step) {
         const int m0 = (t % mtiles) * kTcBM, t0 = (t / mtiles) * NB;
         bool ok = true;
-        for (int kb = 0; kb < nkb; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!tc_wait(&empty[s], ph ^ 1u, &s_abort, a.wait_limit)) {
             ok = false;
             break;
@@ -286,14 +363,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int s = 0, c = 0;
       uint32_t ph = 0, pc = 0;
       bool issued_any = false;
-      for (int t = blockIdx.x; t < tiles && !s_abort; t += gridDim.x) {
+      for (int t = tile0; t < tiles && !s_abort; t += step) {
         const int t0 = (t / mtiles) * NB, n = a.T - t0 < NB ? a.T - t0 : NB;
         const uint32_t idesc = idesc_s8(kTcBM, (n + 31) & ~31);
         if (!tc_wait(&accempty[c], pc ^ 1u, &s_abort, a.wait_limit)) break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(c * NB);
         bool ok = true;
-        for (int kb = 0; kb < nkb; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           const uint64_t ad = sw128_desc(smem_addr(base + s * kStage));
           const uint64_t bd = sw128_desc(smem_addr(base + s * kStage + kTcBM * kTcBK));
           if (!tc_wait(&full[s], ph, &s_abort, a.wait_limit)) {
@@ -302,7 +379,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < kTcBK / 32; ++k) umma_s8(d, ad + 2 * k, bd + 2 * k, idesc, (kb | k) != 0 ? 1u : 0u);
+          for (int k = 0; k < kTcBK / 32; ++k) umma_s8(d, ad + 2 * k, bd + 2 * k, idesc, (kb - kb0) | k ? 1u : 0u);
           issued_any = true;
           umma_commit(&empty[s]);
           if (++s == kStages) {
@@ -328,20 +405,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     float* xs = s_xs[warp - kTcEpiWarp0];
     int c = 0;
     uint32_t pc = 0;
-    for (int t = blockIdx.x; t < tiles && !s_abort; t += gridDim.x) {
+    for (int t = tile0; t < tiles && !s_abort; t += step) {
       const int n = (t % mtiles) * kTcBM + 32 * q + lane, t0 = (t / mtiles) * NB;
       const float ws = n < a.N ? a.ws[n] : 0.0f;
       if (!tc_wait(&accfull[c], pc, &s_abort, a.wait_limit)) break;
       tc_fence_after();
       for (int col = 32 * half; col < NB && t0 + col < a.T; col += 64) {
         uint32_t v[32];
-        __syncwarp();
-        xs[lane] = t0 + col + lane < a.T ? im_token_scale(a, t0 + col + lane) : 0.0f;
-        __syncwarp();
-        tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(c * NB + col), v);
+        if constexpr (SPLIT) {
+          tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(c * NB + col), v);
+          int* red = reinterpret_cast<int*>(base) + col * kTcBM + 32 * q + lane;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (n < a.N && t0 + col + i < a.T) im_store(a, t0 + col + i, n, im_scaled((int)v[i], xs[i], ws));
+          for (int i = 0; i < 32; ++i) red[i * kTcBM] = (int)v[i];
+        } else {
+          const int cnt = a.T - t0 - col;
+          __syncwarp();
+          xs[lane] = lane < cnt ? im_token_scale(a, t0 + col + lane) : 0.0f;
+          __syncwarp();
+          tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(c * NB + col), v);
+          if (cnt >= 32)
+            im_store_chunk<true>(a, v, xs, ws, n, t0 + col, 32, pairs);
+          else
+            im_store_chunk<false>(a, v, xs, ws, n, t0 + col, cnt, pairs);
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -353,6 +439,46 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   }
   pdl_launch_dependents();
+  if constexpr (SPLIT) {
+    // every CTA of the cluster comes here, also after a wait that ran out
+    cluster_sync();
+    const int m0 = (tile0 % mtiles) * kTcBM, t0 = (tile0 / mtiles) * NB, n = a.T - t0 < NB ? a.T - t0 : NB;
+    const bool quads = !(a.N & 3) && !(reinterpret_cast<uintptr_t>(a.y) & 15) &&
+                       !(reinterpret_cast<uintptr_t>(a.add) & 15) && m0 + 4 * lane < a.N;
+    float ws[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ws[i] = m0 + 4 * lane + i < a.N ? a.ws[m0 + 4 * lane + i] : 0.0f;
+    for (int j = rank + split * warp; j < n; j += split * (kTcThreads / 32)) {
+      const float xs = im_token_scale(a, t0 + j);
+      int4 sum = make_int4(0, 0, 0, 0);
+      for (int r = 0; r < split; ++r) {
+        const int4 v = ld_cluster(smem_addr(base) + (uint32_t)(j * kTcBM + 4 * lane) * 4, (uint32_t)r);
+        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+      }
+      float4 f = make_float4(im_scaled(sum.x, xs, ws[0]), im_scaled(sum.y, xs, ws[1]), im_scaled(sum.z, xs, ws[2]),
+                             im_scaled(sum.w, xs, ws[3]));
+      const int64_t at = (int64_t)(t0 + j) * a.N + m0 + 4 * lane;
+      if (quads) {
+        if (a.add) {
+          const float4 d = *reinterpret_cast<const float4*>(a.add + at);
+          f.x += d.x, f.y += d.y, f.z += d.z, f.w += d.w;
+        }
+        if (a.y_f32) {
+          *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) = f;
+        } else {
+          __nv_bfloat162* y = reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(a.y) + at);
+          y[0] = __floats2bfloat162_rn(f.x, f.y);
+          y[1] = __floats2bfloat162_rn(f.z, f.w);
+        }
+      } else {
+        const float fv[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (m0 + 4 * lane + i < a.N) im_store(a, t0 + j, m0 + 4 * lane + i, fv[i]);
+      }
+    }
+    cluster_sync();  // no CTA leaves while another reads its shared memory
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -390,16 +516,34 @@ bool encode_rows(CUtensorMap* m, const int8_t* p, int n, int K, int rows) {
 
 template <int NB>
 cudaError_t launch_tc(const IntMatmulArgs& a, int num_sms, cudaStream_t st) {
-  static int smem_set[4] = {0, 0, 0, 0};
-  const void* kern = reinterpret_cast<const void*>(im_tc_kernel<NB>);
-  cudaError_t e = ensure_smem_attr(kern, smem_set);
+  static int smem_set[2][4] = {};
+  const int mtiles = (a.N + kTcBM - 1) / kTcBM, ntiles = (a.T + NB - 1) / NB;
+  const int64_t tiles = (int64_t)mtiles * ntiles;
+  const int nkb = (a.K + kTcBK - 1) / kTcBK;
+  int split = 1;  // CTAs that share a tile's K, each with two stages of it at least
+  if (NB <= kTcSplitMaxTokens && tiles * 2 <= kTcSplitCtas)
+    split = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(8, kTcSplitCtas / tiles), nkb / 2));
+  const void* kern = split > 1 ? reinterpret_cast<const void*>(im_tc_kernel<NB, NB <= kTcSplitMaxTokens>)
+                               : reinterpret_cast<const void*>(im_tc_kernel<NB, false>);
+  cudaError_t e = ensure_smem_attr(kern, smem_set[split > 1]);
   if (e != cudaSuccess) return e;
   CUtensorMap tw, tx;
   if (!encode_rows(&tw, a.wq, a.N, a.K, kTcBM) || !encode_rows(&tx, a.xq, a.T, a.K, NB)) return cudaErrorInvalidValue;
-  const int mtiles = (a.N + kTcBM - 1) / kTcBM, ntiles = (a.T + NB - 1) / NB;
-  const int64_t tiles = (int64_t)mtiles * ntiles;
-  return launch_pdl(kern, (int)(tiles < num_sms ? tiles : num_sms), kTcThreads, tc_smem_bytes(NB), st, tw, tx, a,
-                    mtiles, ntiles);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(split > 1 ? tiles * split : std::min<int64_t>(tiles, num_sms)));
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = tc_smem_bytes(NB);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {(unsigned)split, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = split > 1 ? 2 : 1;
+  void* argv[] = {&tw, &tx, const_cast<IntMatmulArgs*>(&a), const_cast<int*>(&mtiles), const_cast<int*>(&ntiles),
+                  &split};
+  return cudaLaunchKernelExC(&cfg, kern, argv);
 }
 
 template <int NT>
@@ -417,10 +561,12 @@ cudaError_t launch_int_matmul(const IntMatmulArgs& a, int num_sms, cudaStream_t 
     const int W = a.K >= 4096 ? 8 : a.K >= 2048 ? 4 : 2;
     return launch_pdl(a.T <= 8 ? rows_kernel<1>(W) : rows_kernel<2>(W), (a.N + 15) / 16, 32 * W, 0, st, a);
   }
-  if (a.T <= 32) return launch_tc<32>(a, num_sms, st);
-  if (a.T <= 64) return launch_tc<64>(a, num_sms, st);
-  if (a.T <= 128) return launch_tc<128>(a, num_sms, st);
-  return launch_tc<256>(a, num_sms, st);
+  // the widest token tile that T fills and that gives every SM a tile
+  auto tiles = [&](int nb) { return (int64_t)((a.N + kTcBM - 1) / kTcBM) * ((a.T + nb - 1) / nb); };
+  if (a.T > 128 && tiles(256) >= num_sms) return launch_tc<256>(a, num_sms, st);
+  if (a.T > 64 && tiles(128) >= num_sms) return launch_tc<128>(a, num_sms, st);
+  if (a.T > 32) return launch_tc<64>(a, num_sms, st);
+  return launch_tc<32>(a, num_sms, st);
 }
 
 }  // namespace moe
