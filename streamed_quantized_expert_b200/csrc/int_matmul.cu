@@ -192,6 +192,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// Limit of the waits for a CTA's own copies and MMAs before it exits: those
+// end within microseconds, so a lowered limit does not cut them short.
+__device__ __forceinline__ long long exit_limit(const IntMatmulArgs& a) {
+  return a.wait_limit > (1ll << 24) ? a.wait_limit : 1ll << 24;
+}
+
 // Bounded wait that also gives up once another role of the CTA has aborted.
 __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                         long long limit_cycles) {
@@ -356,7 +362,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!ok) break;
       }
       for (int q = 0; q < kStages; ++q)  // every copy issued lands before the CTA can exit
-        if ((issued >> q) & 1u) mbar_wait_bounded(&full[q], (last_ph >> q) & 1u, a.wait_limit);
+        if ((issued >> q) & 1u) mbar_wait_bounded(&full[q], (last_ph >> q) & 1u, exit_limit(a));
     }
   } else if (warp == kTcMmaWarp) {
     if (lane == 0) {
@@ -396,7 +402,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (issued_any) {  // every MMA issued completes before TMEM is freed
         umma_commit(drain);
-        mbar_wait_bounded(drain, 0, a.wait_limit);
+        mbar_wait_bounded(drain, 0, exit_limit(a));
       }
     }
   } else if (warp >= kTcEpiWarp0) {
@@ -488,6 +494,210 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
+// two CTAs per tile
+// ---------------------------------------------------------------------------
+// Tiles of 256 outputs x 256 tokens on pairs of SMs (cta_group::2): each CTA
+// brings 128 outputs and 128 tokens per stage and keeps the accumulators of
+// its 128 outputs, and one thread of the pair's first CTA issues the MMAs of
+// both.  A 128 x 256 tile of one CTA moves 48 KB from L2 per 128 inputs and
+// measured 53 bytes a clock and SM there, which bounded it; the pair moves
+// 32 KB per CTA for the same MMAs.
+constexpr int kPairBM = 256, kPairBN = 256, kPairStages = 6;
+constexpr int kPairStage = (kPairBM + kPairBN) / 2 * kTcBK;  // bytes of a CTA's share of a stage
+constexpr int kPairSmem = kPairStages * kPairStage + 1024 + 256;
+
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t ra;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(saddr), "r"(rank));
+  return ra;
+}
+// A load into this CTA's shared memory that completes on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* tm, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(smem_addr(dst)),
+      "l"(tm), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void umma_s8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs once the MMAs issued so far are complete.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_addr(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__global__ void __launch_bounds__(kTcThreads, 1)
+    im_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                   const IntMatmulArgs a, const int mtiles, const int ntiles) {
+  extern __shared__ uint8_t im_smem[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(im_smem) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(base + kPairStages * kPairStage);  // both CTAs' TMA -> MMA (CTA 0's)
+  uint64_t* empty = full + kPairStages;   // MMA -> TMA (each CTA's)
+  uint64_t* accfull = empty + kPairStages;  // MMA -> epilogue (each CTA's)
+  uint64_t* accempty = accfull + 2;         // both CTAs' epilogues -> MMA (CTA 0's)
+  uint64_t* drain = accempty + 2;           // MMA at exit (CTA 0's)
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  __shared__ float s_xs[kTcEpiWarps][32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  if (tid == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int c = 0; c < 2; ++c) {
+      mbar_init(&accfull[c], 1);
+      mbar_init(&accempty[c], 2 * kTcEpiWarps);
+    }
+    mbar_init(drain, 1);
+    fence_barrier_init();
+    s_abort = 0;
+    tmap_prefetch(&tm_w);
+    tmap_prefetch(&tm_x);
+  }
+  if (warp == kTcMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&s_tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the pair's barriers exist before either CTA's copies or arrivals reach them
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const int nkb = (a.K + kTcBK - 1) / kTcBK, tiles = mtiles * ntiles;
+  const int tile0 = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const bool pairs = !(a.N & 1) && !(reinterpret_cast<uintptr_t>(a.y) & 3);
+  pdl_wait();
+
+  if (warp == kTcProdWarp) {
+    if (lane == 0) {
+      asm volatile("fence.proxy.async.global;" ::: "memory");  // rows that earlier kernels wrote, to TMA's reads
+      int s = 0;
+      uint32_t ph = 0, issued = 0;
+      for (int t = tile0; t < tiles && !s_abort; t += step) {
+        const int m0 = (t % mtiles) * kPairBM + 128 * (int)rank, t0 = (t / mtiles) * kPairBN + 128 * (int)rank;
+        bool ok = true;
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!tc_wait(&empty[s], ph ^ 1u, &s_abort, a.wait_limit)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = base + s * kPairStage;
+          const uint32_t bar = map_rank(smem_addr(&full[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPairStage);
+          tma_load_2d_pair(st, &tm_w, kb * kTcBK, m0, bar);
+          tma_load_2d_pair(st + 128 * kTcBK, &tm_x, kb * kTcBK, t0, bar);
+          issued |= 1u << s;
+          if (++s == kPairStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+      }
+      // every copy issued lands, and is read, before the CTA can exit: its stage's next emptying says so
+      for (int q = 0; q < kPairStages; ++q) {
+        const uint32_t last = s > q ? ph : ph ^ 1u;  // phase in which stage q was last filled
+        if (((issued >> q) & 1u) && !mbar_wait_bounded(&empty[q], last, exit_limit(a))) break;
+      }
+    }
+  } else if (warp == kTcMmaWarp) {
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = idesc_s8(kPairBM, kPairBN);
+      int s = 0, c = 0;
+      uint32_t ph = 0, pc = 0;
+      bool issued_any = false;
+      for (int t = tile0; t < tiles && !s_abort; t += step) {
+        if (!tc_wait(&accempty[c], pc ^ 1u, &s_abort, a.wait_limit)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(c * kPairBN);
+        bool ok = true;
+        for (int kb = 0; kb < nkb; ++kb) {
+          const uint64_t ad = sw128_desc(smem_addr(base + s * kPairStage));
+          const uint64_t bd = sw128_desc(smem_addr(base + s * kPairStage + 128 * kTcBK));
+          if (!tc_wait(&full[s], ph, &s_abort, a.wait_limit)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < kTcBK / 32; ++k) umma_s8_pair(d, ad + 2 * k, bd + 2 * k, idesc, kb | k ? 1u : 0u);
+          issued_any = true;
+          umma_commit_pair(&empty[s]);
+          if (++s == kPairStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit_pair(&accfull[c]);
+        if (++c == 2) {
+          c = 0;
+          pc ^= 1u;
+        }
+      }
+      if (issued_any) {  // every MMA issued completes before TMEM is freed
+        umma_commit_pair(drain);
+        mbar_wait_bounded(drain, 0, exit_limit(a));
+      }
+    }
+  } else if (warp >= kTcEpiWarp0) {
+    const int q = warp & 3, half = (warp - kTcEpiWarp0) >> 2;
+    float* xs = s_xs[warp - kTcEpiWarp0];
+    int c = 0;
+    uint32_t pc = 0;
+    for (int t = tile0; t < tiles && !s_abort; t += step) {
+      const int n = (t % mtiles) * kPairBM + 128 * (int)rank + 32 * q + lane, t0 = (t / mtiles) * kPairBN;
+      const float ws = n < a.N ? a.ws[n] : 0.0f;
+      if (!tc_wait(&accfull[c], pc, &s_abort, a.wait_limit)) break;
+      tc_fence_after();
+      for (int col = 32 * half; col < kPairBN && t0 + col < a.T; col += 64) {
+        uint32_t v[32];
+        const int cnt = a.T - t0 - col;
+        __syncwarp();
+        xs[lane] = lane < cnt ? im_token_scale(a, t0 + col + lane) : 0.0f;
+        __syncwarp();
+        tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(c * kPairBN + col), v);
+        if (cnt >= 32)
+          im_store_chunk<true>(a, v, xs, ws, n, t0 + col, 32, pairs);
+        else
+          im_store_chunk<false>(a, v, xs, ws, n, t0 + col, cnt, pairs);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_rank(smem_addr(&accempty[c]), 0));
+      if (++c == 2) {
+        c = 0;
+        pc ^= 1u;
+      }
+    }
+  }
+  pdl_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other's copies, MMAs or arrivals may reach it
+  tc_fence_after();
+  if (s_abort && tid == 0 && a.dev_err) atomicOr(a.dev_err, MOE_DEV_ERR_TIMEOUT);
+  if (warp == kTcMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
@@ -546,6 +756,31 @@ cudaError_t launch_tc(const IntMatmulArgs& a, int num_sms, cudaStream_t st) {
   return cudaLaunchKernelExC(&cfg, kern, argv);
 }
 
+cudaError_t launch_pair(const IntMatmulArgs& a, int num_sms, cudaStream_t st) {
+  static int smem_set[4] = {};
+  const void* kern = reinterpret_cast<const void*>(im_pair_kernel);
+  cudaError_t e = ensure_smem_attr(kern, smem_set);
+  if (e != cudaSuccess) return e;
+  CUtensorMap tw, tx;
+  if (!encode_rows(&tw, a.wq, a.N, a.K, 128) || !encode_rows(&tx, a.xq, a.T, a.K, 128)) return cudaErrorInvalidValue;
+  const int mtiles = (a.N + kPairBM - 1) / kPairBM, ntiles = (a.T + kPairBN - 1) / kPairBN;
+  const int64_t pairs = std::min<int64_t>((int64_t)mtiles * ntiles, num_sms / 2);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {2, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  void* argv[] = {&tw, &tx, const_cast<IntMatmulArgs*>(&a), const_cast<int*>(&mtiles), const_cast<int*>(&ntiles)};
+  return cudaLaunchKernelExC(&cfg, kern, argv);
+}
+
 template <int NT>
 const void* rows_kernel(int W) {
   return W == 8   ? reinterpret_cast<const void*>(im_rows_kernel<NT, 8>)
@@ -563,6 +798,7 @@ cudaError_t launch_int_matmul(const IntMatmulArgs& a, int num_sms, cudaStream_t 
   }
   // the widest token tile that T fills and that gives every SM a tile
   auto tiles = [&](int nb) { return (int64_t)((a.N + kTcBM - 1) / kTcBM) * ((a.T + nb - 1) / nb); };
+  if (a.T > 128 && tiles(256) >= num_sms) return launch_pair(a, num_sms, st);
   if (a.T > 128 && tiles(256) >= num_sms) return launch_tc<256>(a, num_sms, st);
   if (a.T > 64 && tiles(128) >= num_sms) return launch_tc<128>(a, num_sms, st);
   if (a.T > 32) return launch_tc<64>(a, num_sms, st);

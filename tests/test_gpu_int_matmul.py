@@ -65,6 +65,7 @@ SIZES = [  # T, N, K: one token to long chunks, odd sizes on both sides of the k
     (33, 257, 144), (48, 5003, 256), (63, 64, 4096), (64, 2048, 512), (65, 100, 128), (100, 384, 8192),
     (127, 127, 1280), (128, 128, 128), (129, 130, 400), (200, 1025, 640), (255, 48, 32), (256, 256, 4096),
     (257, 640, 368), (300, 31, 65536), (513, 1100, 1024), (700, 2049, 528), (2048, 384, 256), (4100, 300, 160),
+    (257, 12801, 1040), (1100, 9000, 272), (2304, 4500, 16),
 ]
 
 
