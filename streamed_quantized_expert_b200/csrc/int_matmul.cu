@@ -136,13 +136,19 @@ __global__ void __launch_bounds__(32 * W, 16 / W) im_rows_kernel(const IntMatmul
 // ---------------------------------------------------------------------------
 constexpr int kTcBM = 128;  // outputs of a tile (MMA M)
 constexpr int kTcBK = 128;  // inputs of a stage: one 128-byte swizzled row per output and token
-constexpr int kTcProdWarp = 0, kTcMmaWarp = 1, kTcEpiWarp0 = 4, kTcEpiWarps = 8;
+constexpr int kTcProdWarp = 0, kTcMmaWarp = 1, kTcEpiWarp0 = 4;
+// the stores of a 128 x 256 tile take 8 warps longer than the MMAs of 512 inputs; a split call's CTAs share an SM
+__host__ __device__ constexpr int tc_epi_warps(bool split) { return split ? 8 : 16; }
+__host__ __device__ constexpr int tc_threads(bool split) { return 32 * (kTcEpiWarp0 + tc_epi_warps(split)); }
 constexpr int kTcSplitMaxTokens = 64;  // token tiles whose K may be split
-constexpr int kTcSplitCtas = 128;      // CTAs of a split call: clusters of up to 8 that 148 SMs take at once
-constexpr int kTcThreads = 32 * (kTcEpiWarp0 + kTcEpiWarps);
+constexpr int kTcSplitCtas = 256;      // CTAs of a split call: clusters of up to 8, two CTAs to an SM
 __host__ __device__ constexpr int tc_stages(int nb) { return nb == 256 ? 4 : nb == 128 ? 6 : 8; }
 __host__ __device__ constexpr int tc_stage_bytes(int nb) { return (kTcBM + nb) * kTcBK; }
-__host__ __device__ constexpr int tc_smem_bytes(int nb) { return tc_stages(nb) * tc_stage_bytes(nb) + 1024 + 256; }
+// a split call's CTAs hold half of an SM's shared memory, so that two of them share it
+__host__ __device__ constexpr int tc_split_stages(int nb) { return nb == 32 ? 4 : 3; }
+__host__ __device__ constexpr int tc_smem_bytes(int nb, int stages, bool split) {
+  return stages * tc_stage_bytes(nb) + 1024 + 256 + (split ? kTcBM * nb * 4 : 0);
+}
 
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* tm, int x, int y, uint64_t* bar) {
   asm volatile(
@@ -226,9 +232,11 @@ __device__ __forceinline__ void im_store_chunk(const IntMatmulArgs& a, const uin
 #pragma unroll
   for (int i0 = 0; i0 < 32; i0 += 8) {
     if (!FULL && i0 >= cnt) break;
+    const float4 x0 = *reinterpret_cast<const float4*>(xs + i0), x1 = *reinterpret_cast<const float4*>(xs + i0 + 4);
+    const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
     float f[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = im_scaled((int)v[i0 + i], xs[i0 + i], ws);
+    for (int i = 0; i < 8; ++i) f[i] = im_scaled((int)v[i0 + i], x[i], ws);
     if (a.add) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -266,51 +274,50 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-// 16 bytes of shared memory of CTA `rank` of the cluster, at this CTA's address `saddr`.
-__device__ __forceinline__ int4 ld_cluster(uint32_t saddr, uint32_t rank) {
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
   uint32_t ra;
-  int4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(saddr), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(ra)
-               : "memory");
-  return v;
+  return ra;
+}
+__device__ __forceinline__ void st_cluster(uint32_t raddr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(raddr), "r"(v) : "memory");
 }
 
 // Tiles of 128 outputs x NB tokens (the outputs' tiles fastest).  Warp 0
-// loads stages by TMA, warp 1 issues the MMAs, warps 4-11 scale and store.
+// loads stages by TMA, warp 1 issues the MMAs, the warps from 4 on scale and store.
 // Inputs past K and rows past N or T arrive as zeros.
 //   SPLIT false: persistent, CTA i takes tiles i, i + grid, ...; accumulators
 //     are double-buffered in TMEM, so that a tile's stores run under the next
 //     one's MMAs.
-//   SPLIT true: one tile per cluster of `split` CTAs, each with its share of
-//     K; their s32 sums meet in shared memory (the stages' space, free by
-//     then), and each CTA finishes every split-th token.
+//   SPLIT true: one tile per cluster of `split` (a power of two) CTAs, each
+//     with its share of K.  Each CTA finishes every split-th token: the others
+//     write their s32 sums of it into its shared memory (stores, which nothing
+//     waits for one by one, where reading them from there measured 2 us more).
 template <int NB, bool SPLIT>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(tc_threads(SPLIT), SPLIT ? 2 : 1)
     im_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
-                 const IntMatmulArgs a, const int mtiles, const int ntiles, const int split) {
+                 const IntMatmulArgs a, const int mtiles, const int ntiles, const int split, const int nst) {
   extern __shared__ uint8_t im_smem[];
-  constexpr int kStages = tc_stages(NB), kStage = tc_stage_bytes(NB), kCols = 2 * NB;
+  constexpr int kEpi = tc_epi_warps(SPLIT), kStage = tc_stage_bytes(NB), kCols = SPLIT ? NB : 2 * NB;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(im_smem) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(base + kStages * kStage);  // TMA -> MMA
-  uint64_t* empty = full + kStages;                                       // MMA -> TMA
-  uint64_t* accfull = empty + kStages;                                    // MMA -> epilogue
+  uint64_t* full = reinterpret_cast<uint64_t*>(base + nst * kStage);  // TMA -> MMA
+  uint64_t* empty = full + nst;                                       // MMA -> TMA
+  uint64_t* accfull = empty + nst;                                    // MMA -> epilogue
   uint64_t* accempty = accfull + 2;                                       // epilogue -> MMA
   uint64_t* drain = accempty + 2;
+  int* red = reinterpret_cast<int*>(base + nst * kStage + 256);  // SPLIT: [source CTA][token / split][output]
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  __shared__ float s_xs[kTcEpiWarps][32];
+  __shared__ __align__(16) float s_xs[kEpi][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < nst; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int c = 0; c < 2; ++c) {
       mbar_init(&accfull[c], 1);
-      mbar_init(&accempty[c], kTcEpiWarps);
+      mbar_init(&accempty[c], kEpi);
     }
     mbar_init(drain, 1);
     fence_barrier_init();
@@ -326,6 +333,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (SPLIT) cluster_sync();  // every CTA of the cluster runs before its shared memory is written to
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   const int nkb = (a.K + kTcBK - 1) / kTcBK, tiles = mtiles * ntiles;
@@ -334,6 +342,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int tile0 = SPLIT ? blockIdx.x / split : blockIdx.x, step = SPLIT ? tiles : gridDim.x;
   const bool pairs = !(a.N & 1) && !(reinterpret_cast<uintptr_t>(a.y) & 3);
   pdl_wait();
+  pdl_launch_dependents();
 
   if (warp == kTcProdWarp) {
     if (lane == 0) {
@@ -354,14 +363,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tma_load_2d(st + kTcBM * kTcBK, &tm_x, kb * kTcBK, t0, &full[s]);
           issued |= 1u << s;
           last_ph = (last_ph & ~(1u << s)) | (ph << s);
-          if (++s == kStages) {
+          if (++s == nst) {
             s = 0;
             ph ^= 1u;
           }
         }
         if (!ok) break;
       }
-      for (int q = 0; q < kStages; ++q)  // every copy issued lands before the CTA can exit
+      for (int q = 0; q < nst; ++q)  // every copy issued lands before the CTA can exit
         if ((issued >> q) & 1u) mbar_wait_bounded(&full[q], (last_ph >> q) & 1u, exit_limit(a));
     }
   } else if (warp == kTcMmaWarp) {
@@ -388,7 +397,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int k = 0; k < kTcBK / 32; ++k) umma_s8(d, ad + 2 * k, bd + 2 * k, idesc, (kb - kb0) | k ? 1u : 0u);
           issued_any = true;
           umma_commit(&empty[s]);
-          if (++s == kStages) {
+          if (++s == nst) {
             s = 0;
             ph ^= 1u;
           }
@@ -406,8 +415,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
   } else if (warp >= kTcEpiWarp0) {
-    // warp i reads TMEM lanes 32 (i % 4)..; the two warps of a quadrant take alternate 32-token chunks
-    const int q = warp & 3, half = (warp - kTcEpiWarp0) >> 2;
+    // warp i reads TMEM lanes 32 (i % 4)..; the warps of a quadrant take 32-token chunks in turn
+    const int q = warp & 3, part = (warp - kTcEpiWarp0) >> 2;
     float* xs = s_xs[warp - kTcEpiWarp0];
     int c = 0;
     uint32_t pc = 0;
@@ -416,13 +425,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const float ws = n < a.N ? a.ws[n] : 0.0f;
       if (!tc_wait(&accfull[c], pc, &s_abort, a.wait_limit)) break;
       tc_fence_after();
-      for (int col = 32 * half; col < NB && t0 + col < a.T; col += 64) {
+      for (int col = 32 * part; col < NB && t0 + col < a.T; col += 8 * kEpi) {
         uint32_t v[32];
         if constexpr (SPLIT) {
           tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(c * NB + col), v);
-          int* red = reinterpret_cast<int*>(base) + col * kTcBM + 32 * q + lane;
+          const uint32_t mine = smem_addr(red) + (uint32_t)((rank * (NB / split)) * kTcBM + 32 * q + lane) * 4;
+          const int lg = __ffs(split) - 1;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) red[i * kTcBM] = (int)v[i];
+          for (int i = 0; i < 32; ++i)
+            if (t0 + col + i < a.T)
+              st_cluster(map_rank(mine + (uint32_t)((col + i) >> lg) * (kTcBM * 4), (uint32_t)(i & (split - 1))), v[i]);
         } else {
           const int cnt = a.T - t0 - col;
           __syncwarp();
@@ -444,21 +456,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
   }
-  pdl_launch_dependents();
   if constexpr (SPLIT) {
-    // every CTA of the cluster comes here, also after a wait that ran out
-    cluster_sync();
+    cluster_sync();  // every CTA of the cluster comes here, also after a wait that ran out
     const int m0 = (tile0 % mtiles) * kTcBM, t0 = (tile0 / mtiles) * NB, n = a.T - t0 < NB ? a.T - t0 : NB;
     const bool quads = !(a.N & 3) && !(reinterpret_cast<uintptr_t>(a.y) & 15) &&
                        !(reinterpret_cast<uintptr_t>(a.add) & 15) && m0 + 4 * lane < a.N;
     float ws[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) ws[i] = m0 + 4 * lane + i < a.N ? a.ws[m0 + 4 * lane + i] : 0.0f;
-    for (int j = rank + split * warp; j < n; j += split * (kTcThreads / 32)) {
+    for (int l = warp; l * split + rank < n; l += kTcEpiWarp0 + kEpi) {
+      const int j = l * split + rank;
       const float xs = im_token_scale(a, t0 + j);
       int4 sum = make_int4(0, 0, 0, 0);
       for (int r = 0; r < split; ++r) {
-        const int4 v = ld_cluster(smem_addr(base) + (uint32_t)(j * kTcBM + 4 * lane) * 4, (uint32_t)r);
+        const int4 v = *reinterpret_cast<const int4*>(red + (r * (NB / split) + l) * kTcBM + 4 * lane);
         sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
       }
       float4 f = make_float4(im_scaled(sum.x, xs, ws[0]), im_scaled(sum.y, xs, ws[1]), im_scaled(sum.z, xs, ws[2]),
@@ -483,7 +494,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (m0 + 4 * lane + i < a.N) im_store(a, t0 + j, m0 + 4 * lane + i, fv[i]);
       }
     }
-    cluster_sync();  // no CTA leaves while another reads its shared memory
   }
   tc_fence_before();
   __syncthreads();
@@ -506,11 +516,6 @@ constexpr int kPairBM = 256, kPairBN = 256, kPairStages = 6;
 constexpr int kPairStage = (kPairBM + kPairBN) / 2 * kTcBK;  // bytes of a CTA's share of a stage
 constexpr int kPairSmem = kPairStages * kPairStage + 1024 + 256;
 
-__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
-  uint32_t ra;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(saddr), "r"(rank));
-  return ra;
-}
 // A load into this CTA's shared memory that completes on a barrier of either CTA of the pair.
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* tm, int x, int y, uint32_t bar) {
   asm volatile(
@@ -539,10 +544,11 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(tc_threads(false), 1)
     im_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                    const IntMatmulArgs a, const int mtiles, const int ntiles) {
   extern __shared__ uint8_t im_smem[];
+  constexpr int kEpi = tc_epi_warps(false);
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(im_smem) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(base + kPairStages * kPairStage);  // both CTAs' TMA -> MMA (CTA 0's)
   uint64_t* empty = full + kPairStages;   // MMA -> TMA (each CTA's)
@@ -551,7 +557,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* drain = accempty + 2;           // MMA at exit (CTA 0's)
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  __shared__ float s_xs[kTcEpiWarps][32];
+  __shared__ __align__(16) float s_xs[kEpi][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   if (tid == 0) {
@@ -561,7 +567,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int c = 0; c < 2; ++c) {
       mbar_init(&accfull[c], 1);
-      mbar_init(&accempty[c], 2 * kTcEpiWarps);
+      mbar_init(&accempty[c], 2 * kEpi);
     }
     mbar_init(drain, 1);
     fence_barrier_init();
@@ -583,6 +589,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int tile0 = blockIdx.x >> 1, step = gridDim.x >> 1;
   const bool pairs = !(a.N & 1) && !(reinterpret_cast<uintptr_t>(a.y) & 3);
   pdl_wait();
+  pdl_launch_dependents();
 
   if (warp == kTcProdWarp) {
     if (lane == 0) {
@@ -657,7 +664,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
   } else if (warp >= kTcEpiWarp0) {
-    const int q = warp & 3, half = (warp - kTcEpiWarp0) >> 2;
+    const int q = warp & 3, part = (warp - kTcEpiWarp0) >> 2;
     float* xs = s_xs[warp - kTcEpiWarp0];
     int c = 0;
     uint32_t pc = 0;
@@ -666,7 +673,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const float ws = n < a.N ? a.ws[n] : 0.0f;
       if (!tc_wait(&accfull[c], pc, &s_abort, a.wait_limit)) break;
       tc_fence_after();
-      for (int col = 32 * half; col < kPairBN && t0 + col < a.T; col += 64) {
+      for (int col = 32 * part; col < kPairBN && t0 + col < a.T; col += 8 * kEpi) {
         uint32_t v[32];
         const int cnt = a.T - t0 - col;
         __syncwarp();
@@ -687,7 +694,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
   }
-  pdl_launch_dependents();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // neither CTA leaves while the other's copies, MMAs or arrivals may reach it
@@ -725,14 +731,12 @@ bool encode_rows(CUtensorMap* m, const int8_t* p, int n, int K, int rows) {
 }
 
 template <int NB>
-cudaError_t launch_tc(const IntMatmulArgs& a, int num_sms, cudaStream_t st) {
+cudaError_t launch_tc(const IntMatmulArgs& a, int split, int num_sms, cudaStream_t st) {
+  while (split & (split - 1)) split &= split - 1;  // a power of two, which the kernel's owners of tokens rely on
   static int smem_set[2][4] = {};
   const int mtiles = (a.N + kTcBM - 1) / kTcBM, ntiles = (a.T + NB - 1) / NB;
   const int64_t tiles = (int64_t)mtiles * ntiles;
   const int nkb = (a.K + kTcBK - 1) / kTcBK;
-  int split = 1;  // CTAs that share a tile's K, each with two stages of it at least
-  if (NB <= kTcSplitMaxTokens && tiles * 2 <= kTcSplitCtas)
-    split = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(8, kTcSplitCtas / tiles), nkb / 2));
   const void* kern = split > 1 ? reinterpret_cast<const void*>(im_tc_kernel<NB, NB <= kTcSplitMaxTokens>)
                                : reinterpret_cast<const void*>(im_tc_kernel<NB, false>);
   cudaError_t e = ensure_smem_attr(kern, smem_set[split > 1]);
@@ -741,8 +745,9 @@ cudaError_t launch_tc(const IntMatmulArgs& a, int num_sms, cudaStream_t st) {
   if (!encode_rows(&tw, a.wq, a.N, a.K, kTcBM) || !encode_rows(&tx, a.xq, a.T, a.K, NB)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(split > 1 ? tiles * split : std::min<int64_t>(tiles, num_sms)));
-  cfg.blockDim = dim3(kTcThreads);
-  cfg.dynamicSmemBytes = tc_smem_bytes(NB);
+  cfg.blockDim = dim3(tc_threads(split > 1));
+  const int nst = split > 1 ? std::min(tc_split_stages(NB), (nkb + split - 1) / split) : tc_stages(NB);
+  cfg.dynamicSmemBytes = tc_smem_bytes(NB, nst, split > 1);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -752,7 +757,7 @@ cudaError_t launch_tc(const IntMatmulArgs& a, int num_sms, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = split > 1 ? 2 : 1;
   void* argv[] = {&tw, &tx, const_cast<IntMatmulArgs*>(&a), const_cast<int*>(&mtiles), const_cast<int*>(&ntiles),
-                  &split};
+                  &split, const_cast<int*>(&nst)};
   return cudaLaunchKernelExC(&cfg, kern, argv);
 }
 
@@ -767,7 +772,7 @@ cudaError_t launch_pair(const IntMatmulArgs& a, int num_sms, cudaStream_t st) {
   const int64_t pairs = std::min<int64_t>((int64_t)mtiles * ntiles, num_sms / 2);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * pairs));
-  cfg.blockDim = dim3(kTcThreads);
+  cfg.blockDim = dim3(tc_threads(false));
   cfg.dynamicSmemBytes = kPairSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -779,6 +784,48 @@ cudaError_t launch_pair(const IntMatmulArgs& a, int num_sms, cudaStream_t st) {
   cfg.numAttrs = 2;
   void* argv[] = {&tw, &tx, const_cast<IntMatmulArgs*>(&a), const_cast<int*>(&mtiles), const_cast<int*>(&ntiles)};
   return cudaLaunchKernelExC(&cfg, kern, argv);
+}
+
+struct TcPlan {
+  int nb, split;  // tokens of a tile (0: 256 x 256 on pairs of SMs), CTAs that share a tile's K
+};
+
+// The tile and split of a call: the least estimated time, in us,
+//   3.6 + rounds x (128-input blocks of a CTA) x block + stores (+ split),
+// where a round is one tile per SM (or pair, or two half-size CTAs per SM of a
+// split call).  Its constants were fitted to every choice timed at 47 sizes
+// (N 1024 to 16384, K 512 to 8192, 17 to 4096 tokens, weights not in L2): the
+// choice is within 8 % of the best one there.  Some of what it decides between:
+//   64 x 1536 x 2048     split 4 ways 4.4 us, whole 7.8
+//   512 x 4096 x 2048    128-token tiles 9.5 us, 64-token tiles (two rounds) 14.5
+//   1024 x 4096 x 8192   pairs 27.4 us, 256-token tiles 30.3, 128-token tiles 44.5
+TcPlan tc_plan(const IntMatmulArgs& a, int num_sms) {
+  static constexpr struct {
+    int nb;
+    float block, stores;
+  } kTile[] = {{32, 0.285f, 0.25f}, {64, 0.30f, 0.4f}, {128, 0.325f, 0.7f}, {256, 0.40f, 2.2f}, {0, 0.36f, 3.0f}};
+  const int nkb = (a.K + kTcBK - 1) / kTcBK;
+  TcPlan best{64, 1};
+  float least = 3e38f;
+  for (const auto& c : kTile) {
+    const int bm = c.nb ? kTcBM : kPairBM, bn = c.nb ? c.nb : kPairBN, slots = c.nb ? num_sms : num_sms / 2;
+    if (bn > 32 && a.T <= bn / 2) break;  // a narrower tile holds every token
+    const int64_t tiles = (int64_t)((a.N + bm - 1) / bm) * ((a.T + bn - 1) / bn);
+    for (int split = 1; split <= 8; split *= 2) {
+      if (split > 1 && (c.nb == 0 || c.nb > kTcSplitMaxTokens || tiles * split > kTcSplitCtas || split > nkb / 2)) break;
+      const int64_t rounds = (tiles * split + slots - 1) / slots;
+      float t = 3.6f + c.stores + (float)rounds * (float)((nkb + split - 1) / split) * c.block;
+      if (split > 1) {
+        t += c.nb == 32 ? 0.2f : 0.9f;
+        if (rounds > 1) t += 0.5f - 0.25f * (float)rounds * (float)((nkb + split - 1) / split) * c.block;  // on one SM
+      }
+      if (t < least) {
+        least = t;
+        best = {c.nb, split};
+      }
+    }
+  }
+  return best;
 }
 
 template <int NT>
@@ -796,13 +843,12 @@ cudaError_t launch_int_matmul(const IntMatmulArgs& a, int num_sms, cudaStream_t 
     const int W = a.K >= 4096 ? 8 : a.K >= 2048 ? 4 : 2;
     return launch_pdl(a.T <= 8 ? rows_kernel<1>(W) : rows_kernel<2>(W), (a.N + 15) / 16, 32 * W, 0, st, a);
   }
-  // the widest token tile that T fills and that gives every SM a tile
-  auto tiles = [&](int nb) { return (int64_t)((a.N + kTcBM - 1) / kTcBM) * ((a.T + nb - 1) / nb); };
-  if (a.T > 128 && tiles(256) >= num_sms) return launch_pair(a, num_sms, st);
-  if (a.T > 128 && tiles(256) >= num_sms) return launch_tc<256>(a, num_sms, st);
-  if (a.T > 64 && tiles(128) >= num_sms) return launch_tc<128>(a, num_sms, st);
-  if (a.T > 32) return launch_tc<64>(a, num_sms, st);
-  return launch_tc<32>(a, num_sms, st);
+  const TcPlan p = tc_plan(a, num_sms);
+  if (p.nb == 32) return launch_tc<32>(a, p.split, num_sms, st);
+  if (p.nb == 64) return launch_tc<64>(a, p.split, num_sms, st);
+  if (p.nb == 128) return launch_tc<128>(a, 1, num_sms, st);
+  if (p.nb == 256) return launch_tc<256>(a, 1, num_sms, st);
+  return launch_pair(a, num_sms, st);
 }
 
 }  // namespace moe
