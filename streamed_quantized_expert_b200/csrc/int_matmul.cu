@@ -514,6 +514,8 @@ __global__ void __launch_bounds__(tc_threads(SPLIT), SPLIT ? 2 : 1)
 // 32 KB per CTA for the same MMAs.
 constexpr int kPairBM = 256, kPairBN = 256, kPairStages = 6;
 constexpr int kPairStage = (kPairBM + kPairBN) / 2 * kTcBK;  // bytes of a CTA's share of a stage
+// eight warps store: sixteen took 4 % longer at K 4096 (99 us against 95), where the stores run under the MMAs
+constexpr int kPairEpiWarps = 8, kPairThreads = 32 * (kTcEpiWarp0 + kPairEpiWarps);
 constexpr int kPairSmem = kPairStages * kPairStage + 1024 + 256;
 
 // A load into this CTA's shared memory that completes on a barrier of either CTA of the pair.
@@ -544,11 +546,11 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-__global__ void __launch_bounds__(tc_threads(false), 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
     im_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                    const IntMatmulArgs a, const int mtiles, const int ntiles) {
   extern __shared__ uint8_t im_smem[];
-  constexpr int kEpi = tc_epi_warps(false);
+  constexpr int kEpi = kPairEpiWarps;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(im_smem) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(base + kPairStages * kPairStage);  // both CTAs' TMA -> MMA (CTA 0's)
   uint64_t* empty = full + kPairStages;   // MMA -> TMA (each CTA's)
@@ -772,7 +774,7 @@ cudaError_t launch_pair(const IntMatmulArgs& a, int num_sms, cudaStream_t st) {
   const int64_t pairs = std::min<int64_t>((int64_t)mtiles * ntiles, num_sms / 2);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * pairs));
-  cfg.blockDim = dim3(tc_threads(false));
+  cfg.blockDim = dim3(kPairThreads);
   cfg.dynamicSmemBytes = kPairSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
