@@ -449,10 +449,11 @@ moe_status moe_quantize_channels(const void* w, int32_t w_type, int32_t rows, in
   if (!w || !q || !scale || !aligned(w, 16) || !aligned(q, 8) || !aligned(scale, 4)) return MOE_ERR_INVALID;
   RowQuantArgs a{};
   a.in = w;
+  a.T = rows;
   a.H = K;
   a.q = q;
   a.scale = scale;
-  return cuda_status(launch_row_quant(a, kRowPlain, w_type == MOE_F32, false, rows, stream));
+  return cuda_status(launch_row_quant(a, kRowPlain, w_type == MOE_F32, false, stream));
 }
 
 moe_status moe_add_norm_quant(const void* h, int32_t h_type, const void* delta, int32_t delta_type,
@@ -471,12 +472,14 @@ moe_status moe_add_norm_quant(const void* h, int32_t h_type, const void* delta, 
   a.delta = delta;
   a.gamma = gamma;
   a.eps = eps;
+  a.inv_h = 1.0f / (float)H;
+  a.T = T;
   a.H = H;
   a.h_out = h_out;
   a.x = x;
   a.q = q;
   a.scale = q_scale;
-  return cuda_status(launch_row_quant(a, kRowNorm, h_type == MOE_F32, delta && delta_type == MOE_F32, T, stream));
+  return cuda_status(launch_row_quant(a, kRowNorm, h_type == MOE_F32, delta && delta_type == MOE_F32, stream));
 }
 
 moe_status moe_swiglu_quant(const void* gu, int32_t gu_type, int32_t T, int32_t I, int8_t* q, float* q_scale,
@@ -487,10 +490,11 @@ moe_status moe_swiglu_quant(const void* gu, int32_t gu_type, int32_t T, int32_t 
   if (!gu || !q || !q_scale || !aligned(gu, 16) || !aligned(q, 8) || !aligned(q_scale, 4)) return MOE_ERR_INVALID;
   RowQuantArgs a{};
   a.in = gu;
+  a.T = T;
   a.H = I;
   a.q = q;
   a.scale = q_scale;
-  return cuda_status(launch_row_quant(a, kRowSwiglu, gu_type == MOE_F32, false, T, stream));
+  return cuda_status(launch_row_quant(a, kRowSwiglu, gu_type == MOE_F32, false, stream));
 }
 
 moe_status moe_int_matmul(const int8_t* xq, const float* x_scale, int32_t T, const int8_t* wq, const float* w_scale,

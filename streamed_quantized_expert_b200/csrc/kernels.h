@@ -93,8 +93,8 @@ struct RowQuantArgs {
   const void* in;         // [T][H], or [T][2H] (SwiGLU: gate columns, then up columns)
   const void* delta;      // norm: [T][H] or null
   const uint16_t* gamma;  // norm: [H]
-  float eps;
-  int H;  // columns of a quantised row
+  float eps, inv_h;       // inv_h: 1 / H
+  int T, H;  // rows and columns of what is quantised
   void* h_out;
   uint16_t* x;
   int8_t* q;
@@ -158,7 +158,7 @@ cudaError_t launch_quantize(const float* w, int rows, int K, int g, int b, int g
 cudaError_t launch_dequant_slot(const uint8_t* slot, const moe_layer_desc& d, const Layout& L, float* out32,
                                 uint16_t* out16, cudaStream_t st);
 cudaError_t launch_route_grouped(const RouteGroupedArgs& a, cudaStream_t st);
-cudaError_t launch_row_quant(const RowQuantArgs& a, int op, bool in_f32, bool delta_f32, int T, cudaStream_t st);
+cudaError_t launch_row_quant(const RowQuantArgs& a, int op, bool in_f32, bool delta_f32, cudaStream_t st);
 cudaError_t launch_int_matmul(const IntMatmulArgs& a, int num_sms, cudaStream_t st);
 bool ffn_decode_supported(const moe_layer_desc& d);
 cudaError_t launch_ffn_decode(FfnArgs a, const moe_layer_desc& d, int num_sms, cudaStream_t st);
