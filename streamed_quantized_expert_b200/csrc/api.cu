@@ -419,6 +419,9 @@ moe_status moe_route_grouped(const float* logits, int32_t T, const moe_layer_des
   if (T == 0) return MOE_OK;
   if (!logits || !ids || !w) return MOE_ERR_INVALID;
   if (L > 0.0f && !slot_table) return MOE_ERR_INVALID;
+  if (!aligned(logits, 4) || !aligned(bias, 4) || !aligned(slot_table, 4) || !aligned(shared_w, 4) ||
+      !aligned(ids, 4) || !aligned(w, 4))
+    return MOE_ERR_INVALID;
   if ((int64_t)T * d->k > (1 << 24)) return MOE_ERR_UNSUPPORTED;
   RouteGroupedArgs a{};
   a.logits = logits;
@@ -438,7 +441,7 @@ moe_status moe_route_grouped(const float* logits, int32_t T, const moe_layer_des
   a.shared_w = shared_w;
   a.ids = ids;
   a.w = w;
-  return cuda_status(launch_route_grouped(a, stream));
+  return cuda_status(launch_route_grouped(a, device_sms(), stream));
 }
 
 moe_status moe_quantize_channels(const void* w, int32_t w_type, int32_t rows, int32_t K, int8_t* q, float* scale,
@@ -504,7 +507,7 @@ moe_status moe_int_matmul(const int8_t* xq, const float* x_scale, int32_t T, con
   if (T > 1 << 20 || N > 1 << 20 || K > 1 << 16) return MOE_ERR_UNSUPPORTED;
   if (T == 0 || N == 0) return MOE_OK;
   if (!xq || !x_scale || !wq || !w_scale || !y || !aligned(xq, 16) || !aligned(wq, 16)) return MOE_ERR_INVALID;
-  if (!aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(add, 4) || !aligned(row_w, 4) ||
+  if (!aligned(dev_err, 4) || !aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(add, 4) || !aligned(row_w, 4) ||
       !aligned(y, y_type == MOE_F32 ? 4 : 2))
     return MOE_ERR_INVALID;
   if (add == y && y_type != MOE_F32) return MOE_ERR_INVALID;

@@ -157,7 +157,7 @@ cudaError_t launch_exp(const float* x, int64_t n, float* out, cudaStream_t st);
 cudaError_t launch_quantize(const float* w, int rows, int K, int g, int b, int gu_I, uint8_t* q, cudaStream_t st);
 cudaError_t launch_dequant_slot(const uint8_t* slot, const moe_layer_desc& d, const Layout& L, float* out32,
                                 uint16_t* out16, cudaStream_t st);
-cudaError_t launch_route_grouped(const RouteGroupedArgs& a, cudaStream_t st);
+cudaError_t launch_route_grouped(const RouteGroupedArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_row_quant(const RowQuantArgs& a, int op, bool in_f32, bool delta_f32, cudaStream_t st);
 cudaError_t launch_int_matmul(const IntMatmulArgs& a, int num_sms, cudaStream_t st);
 bool ffn_decode_supported(const moe_layer_desc& d);

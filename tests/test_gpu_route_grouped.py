@@ -185,3 +185,52 @@ def test_another_stream_and_a_replayed_graph():
         g.replay()
         torch.cuda.synchronize()
         assert np.array_equal(ids.cpu().numpy(), ref.route(logits, k, True, bias, 8, 4, 2)[0])
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,G,top,gtop", [(32, 8, 1, 1, 1), (100, 20, 1, 1, 1), (256, 8, 8, 3, 2), (512, 31, 1, 1, 1),
+                                            (512, 32, 4, 2, 2), (1024, 16, 32, 7, 1)])
+@pytest.mark.parametrize("L", [0.0, 0.125])
+def test_choices_below_fp32(score, E, k, G, top, gtop, L):
+    """A bias that takes every token-0 score to 1 up to its own rounding (some
+    2^-25): experts and groups are told apart by what fp32 does not hold.  The
+    other tokens have some such pairs or none."""
+    r = np.random.default_rng(E + k)
+    T = 9
+    logits = r.standard_normal((T, E)).astype(np.float32)
+    l64 = logits[0].astype(np.float64)
+    s = 1 / (1 + np.exp(-l64)) if score == "sigmoid" else np.exp(l64 - l64.max()) / np.exp(l64 - l64.max()).sum()
+    bias = (1.0 - s).astype(np.float32)
+    logits[1, :E // 2] = logits[0, :E // 2]                    # half of the pairs (the softmax's sum is another)
+    logits[2] = logits[0][::-1]
+    logits[3] = np.nextafter(logits[0], np.float32(9))
+    logits[4] = np.float32(0.5)
+    table = np.where(r.random(E) < 0.5, r.integers(0, 9, E), -1).astype(np.int32)
+    check(logits, k, score, bias, G, top, gtop, True, 1.0, L, table)
+    # pairs of equal experts at the border of the choice
+    bias[1::2] = bias[::2]
+    logits[:, 1::2] = logits[:, ::2]
+    check(logits, k, score, bias, G, top, gtop, False, 1.0, L, np.repeat(table[::2], 2)[:E])
+
+
+@pytest.mark.parametrize("lmax", [1e3, 1e5, 3e38])
+def test_large_logits(lmax):
+    r = np.random.default_rng(2)
+    logits = (lmax * r.uniform(-1, 1, (6, 96))).astype(np.float32)
+    for score in ("softmax", "sigmoid"):
+        for bias in (None, (0.1 * r.standard_normal(96)).astype(np.float32)):
+            for renorm in (True, False):
+                check(logits, 5, score, bias, 8, 4, 2, renorm)
+
+
+def test_logits_at_an_odd_address():
+    """Rows that start 4-byte aligned only."""
+    T, E, k = 7, 256, 8
+    logits = synth.router_logits(8, 0, T, E)
+    buf = torch.zeros(T * E + 3, device="cuda")
+    buf[3:] = dev(logits).reshape(-1)
+    d = ops.desc(E, k, 64, 32, 32, 4)
+    ids, w = torch.zeros((T, k), dtype=torch.int32, device="cuda"), torch.zeros((T, k), device="cuda")
+    ops.moe_route_grouped(buf[3:], T, d, ops.route_config("sigmoid", 8, 4, 2), None, 0.0, None, 0, None, ids, w)
+    torch.cuda.synchronize()
+    assert np.array_equal(ids.cpu().numpy(), ref.route(logits, k, True, None, 8, 4, 2)[0])

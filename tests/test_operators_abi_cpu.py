@@ -57,6 +57,8 @@ def test_struct_size():
     (INV, dict(d=ops.desc(64, 65, 64, 32, 32, 4)), dict()),
     (UNS, dict(d=ops.desc(2048, 4, 64, 32, 32, 4)), dict()),
     (UNS, dict(T=(1 << 22) + 1), dict()),
+    (INV, dict(logits=P + 1), dict()), (INV, dict(bias=P + 2), dict()), (INV, dict(L=0.5, table=P + 2), dict()),
+    (INV, dict(ns=1, sw=P + 3), dict()), (INV, dict(ids=P + 1), dict()), (INV, dict(w=P + 2), dict()),
 ])
 def test_route_refusals(status, kw, cfg):
     c = None if cfg is None else ops.route_config(**cfg)
@@ -110,6 +112,7 @@ def mm(xq=P, xs=P, T=4, wq=P, ws=P, N=64, K=64, add=None, row_w=None, y=P, yt=0,
     (UNS, dict(T=(1 << 20) + 1)), (UNS, dict(N=(1 << 20) + 1)), (INV, dict(yt=2)),
     (INV, dict(xq=P + 8)), (INV, dict(wq=P + 1)), (INV, dict(xs=P + 2)), (INV, dict(y=P + 1)),
     (INV, dict(yt=1, y=P + 2)), (INV, dict(add=P + 2)), (INV, dict(row_w=P + 1)),
+    (INV, dict(err=P + 2)),
     (INV, dict(add=P, y=P, yt=0)),  # in place only where y is fp32
 ])
 def test_int_matmul_refusals(status, kw):
