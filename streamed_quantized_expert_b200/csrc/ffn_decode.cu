@@ -404,8 +404,17 @@ __global__ void combine_kernel(const FfnArgs a) {
   const int64_t w0 = (int64_t)((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
   const int64_t nw = (int64_t)((gridDim.x * blockDim.x) >> 5);
   const int nch = (a.H + kCombineChunk - 1) / kCombineChunk;
+  // the pass's experts: its list need not be a range of ids (a decode layer
+  // with misses runs [resident..., installed...] as two passes)
+  __shared__ uint32_t s_pass[32];  // one bit per expert (E <= 1024)
   const int n_act = pass_count(a);
-  const int e_lo = n_act > 0 ? a.active[a.pass_begin] : 1, e_hi = n_act > 0 ? a.active[a.pass_begin + n_act - 1] : 0;
+  if (threadIdx.x < 32) s_pass[threadIdx.x] = 0u;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n_act; i += blockDim.x) {
+    const unsigned e = (unsigned)a.active[a.pass_begin + i];
+    if (e < 1024u) atomicOr(&s_pass[e >> 5], 1u << (e & 31));
+  }
+  __syncthreads();
   const bool vec = (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
   for (int64_t it = w0; it < (int64_t)a.T * nch; it += nw) {
     const int t = (int)(it / nch), ch = (int)(it % nch);
@@ -413,8 +422,8 @@ __global__ void combine_kernel(const FfnArgs a) {
     float wj = 0.f;
     if (lane < a.k) {
       const int pf = t * a.k + lane;
-      const int e = a.ids[pf];
-      in = e >= e_lo && e <= e_hi && slot_ok(a, a.table[e]);
+      const unsigned e = (unsigned)a.ids[pf];
+      in = e < 1024u && ((s_pass[e >> 5] >> (e & 31)) & 1u) && slot_ok(a, a.table[e]);
       wj = a.w[pf];
     }
     const unsigned mask = __ballot_sync(0xffffffffu, in);
