@@ -591,7 +591,13 @@ typedef struct {
                                    table_dev then has E + n_shared entries and the step buffers
                                    are sized for E + n_shared experts, k + n_shared per token */
   const float* shared_w;        /* device fp32 [T] per-token weight of the shared experts, or NULL (1) */
+  const moe_route_config* route; /* how the layer routes (moe_route_grouped), or NULL: moe_route */
+  const float* route_bias;      /* device fp32 [E], the bias of moe_route_grouped, or NULL */
 } moe_layer_ctx;
+
+/* (A layer with `route` set takes moe_route_grouped where the calls below say
+ * moe_route or moe_route_shared, and for one token the separate sort and
+ * lookup; its guesses, too.) */
 
 /* One decode layer, T <= 64 tokens (RFC "How the prototype works": each layer
  * copies its routing to the host once; misses cost one host-to-device copy

@@ -144,6 +144,16 @@ moe_status retire(moe_prefetch* pf, moe_cache* cache, int32_t layer, const moe_l
   return MOE_OK;
 }
 
+// A layer's routing, with ns shared experts: by its own router configuration if it has one.
+moe_status route_layer(const moe_layer_ctx* lc, const float* logits, int32_t T, float L, const int32_t* table,
+                       int32_t ns, int32_t* ids, float* w, cudaStream_t stream) {
+  if (lc->route)
+    return moe_route_grouped(logits, T, lc->desc, lc->route, lc->route_bias, L, table, ns, lc->shared_w, ids, w,
+                             stream);
+  return ns ? moe_route_shared(logits, T, lc->desc, L, table, ns, lc->shared_w, ids, w, stream)
+            : moe_route(logits, T, lc->desc, L, table, ids, w, stream);
+}
+
 // The guessed layers' experts (ids back on the host): reserve slots for the
 // misses and start their copies on the ahead stream.
 moe_status start_guesses(const Guess& G, moe_cache* cache, int32_t T) {
@@ -209,8 +219,8 @@ moe_status decode_layer(moe_cache* cache, int32_t layer, const moe_layer_ctx* lc
   // experts always), it reads x sorted by expert
   uint16_t* xs =
       (b->x_sorted && moe_ffn_kernel_path(d, T, 1) == MOE_PATH_TC_PREFILL) ? b->x_sorted : nullptr;
-  // one token without sorted x: routing, sort and lookup in one launch
-  const bool one = T == 1 && !xs;
+  // one token without sorted x: routing (moe_route's), sort and lookup in one launch
+  const bool one = T == 1 && !xs && !lc->route;
   if (one && ns == 0 && !(G && G->n > 0) && moe_cache_resident(cache, layer) >= E0) {
     // a fully resident layer: the FFN launch routes the token itself (the host needs none of it)
     const moe_status r = moe_route_expert_ffn(x, logits, T, d0, L, lc->pool, lc->n_slots, lc->table_dev, b->ids,
@@ -235,8 +245,7 @@ moe_status decode_layer(moe_cache* cache, int32_t layer, const moe_layer_ctx* lc
                                        b->dev_err, stream, host_meta, seq);
     if (s != MOE_OK) return s;
   } else {
-    s = ns ? moe_route_shared(logits, T, d0, L, lc->table_dev, ns, lc->shared_w, b->ids, b->w, stream)
-           : moe_route(logits, T, d0, L, lc->table_dev, b->ids, b->w, stream);
+    s = route_layer(lc, logits, T, L, lc->table_dev, ns, b->ids, b->w, stream);
     if (s != MOE_OK) return s;
     s = moe_sort(b->ids, xs ? x : nullptr, T, d, b->offsets, b->pairs, active, n_active, xs, b->ws, b->ws_bytes,
                  stream);
@@ -247,7 +256,7 @@ moe_status decode_layer(moe_cache* cache, int32_t layer, const moe_layer_ctx* lc
     for (int32_t gi = 0; gi < G->n; ++gi) {
       const moe_guess& g = G->g[gi];
       int32_t* gids = G->gb->ids + (size_t)gi * G->gb->stride;
-      s = moe_route(g.logits, T, g.lc->desc, 0.0f, nullptr, gids, G->gb->w + (size_t)gi * G->gb->stride, stream);
+      s = route_layer(g.lc, g.logits, T, 0.0f, nullptr, 0, gids, G->gb->w + (size_t)gi * G->gb->stride, stream);
       if (s != MOE_OK) return s;
       if (cudaMemcpyAsync(G->gb->ids_host + (size_t)gi * G->gb->stride, gids,
                           sizeof(int32_t) * (size_t)T * g.lc->desc->k, cudaMemcpyDeviceToHost, stream) != cudaSuccess)

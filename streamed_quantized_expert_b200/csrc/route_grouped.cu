@@ -267,7 +267,7 @@ __device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const floa
   }
   if (__any_sync(kAll, !(big < INFINITY))) return false;  // an expert that is off, or a logit without order
   M = sum = 0.0f;
-  float D = 0.0f, inv = 1.0f, lift = 0.0f, hi = -INFINITY, lo = -INFINITY;  // lo: of -c at first
+  float D = 0.0f, inv = 1.0f, lift = 0.0f, most = 0.0f, hi = -INFINITY, lo = -INFINITY;  // lo: of -c at first
   if (!a.sigmoid) {
     M = warp_max(lmax) * kLog2e;
     if (!(fabsf(M) < 65536.0f)) return false;  // its rounding, which all terms share, would leave 2^x's range
@@ -324,7 +324,8 @@ __device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const floa
         if ((resident >> i) & 1u) s[i] = __fadd_rn(s[i], lift);
     }
     // the sums with the bias and the lift round to steps of the largest of them
-    D = unit * (1.0f + 2.0f * a.L) + 0x1p-22f * (fmaxf(fabsf(hi), fabsf(lo)) + lift);
+    most = fmaxf(fabsf(hi), fabsf(lo));
+    D = lifted ? unit * (1.0f + 2.0f * a.L) + 0x1p-22f * (most + lift) : unit + 0x1.1p-24f * most;
     if (groups) {
       if constexpr (FULL) {
 #pragma unroll
@@ -367,7 +368,8 @@ __device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const floa
     const bool kept = g < a.G && better < a.top;
     const uint32_t lanes_kept = __ballot_sync(kAll, kept);
     const float low = warp_min(kept ? mine : INFINITY), high = warp_max(g < a.G && !kept ? mine : -INFINITY);
-    if (!(low - high > 5.0f * D)) return false;
+    // the sum of two c is off by 2 D and its own rounding
+    if (!(low - high > 4.0f * D + 0x1p-22f * (most + lift))) return false;
     const uint32_t inv_m = ((1u << 22) + m - 1) / m;  // e / m = e inv_m >> 22 for e < 1024
     const bool fours = FULL && (m & 3) == 0;          // four experts side by side share a group
 #pragma unroll

@@ -57,20 +57,6 @@ class StepBuffers(C.Structure):
                 ("x_sorted", C.c_void_p)]
 
 
-class LayerCtx(C.Structure):
-    _fields_ = [("desc", C.POINTER(LayerDesc)), ("pool", C.c_void_p), ("n_slots", C.c_int32),
-                ("slot_bytes", C.c_size_t), ("table_dev", C.c_void_p), ("table_stage", C.c_void_p),
-                ("bank_rows", C.POINTER(C.c_void_p)), ("n_shared", C.c_int32), ("shared_w", C.c_void_p)]
-
-
-class Guess(C.Structure):
-    _fields_ = [("layer", C.c_int32), ("lc", C.POINTER(LayerCtx)), ("logits", C.c_void_p), ("top", C.c_int32)]
-
-
-class GuessBuffers(C.Structure):
-    _fields_ = [("ids", C.c_void_p), ("w", C.c_void_p), ("ids_host", C.c_void_p), ("stride", C.c_int32)]
-
-
 class RouteConfig(C.Structure):
     """How moe_route_grouped scores and chooses (moe_route_config)."""
     _fields_ = [("score", C.c_int32), ("n_groups", C.c_int32), ("top_groups", C.c_int32), ("group_top", C.c_int32),
@@ -79,6 +65,21 @@ class RouteConfig(C.Structure):
     def __repr__(self):
         return (f"RouteConfig(score={self.score}, n_groups={self.n_groups}, top_groups={self.top_groups}, "
                 f"group_top={self.group_top}, renormalise={self.renormalise}, scale={self.scale})")
+
+
+class LayerCtx(C.Structure):
+    _fields_ = [("desc", C.POINTER(LayerDesc)), ("pool", C.c_void_p), ("n_slots", C.c_int32),
+                ("slot_bytes", C.c_size_t), ("table_dev", C.c_void_p), ("table_stage", C.c_void_p),
+                ("bank_rows", C.POINTER(C.c_void_p)), ("n_shared", C.c_int32), ("shared_w", C.c_void_p),
+                ("route", C.POINTER(RouteConfig)), ("route_bias", C.c_void_p)]
+
+
+class Guess(C.Structure):
+    _fields_ = [("layer", C.c_int32), ("lc", C.POINTER(LayerCtx)), ("logits", C.c_void_p), ("top", C.c_int32)]
+
+
+class GuessBuffers(C.Structure):
+    _fields_ = [("ids", C.c_void_p), ("w", C.c_void_p), ("ids_host", C.c_void_p), ("stride", C.c_int32)]
 
 
 class SlotLayout(C.Structure):

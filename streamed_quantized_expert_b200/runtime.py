@@ -13,6 +13,10 @@ device pool and one LRU range per (class, layer) (1bit-MONSTER PR #137).
 Always-on shared experts (BigMoeOnEdge docs/limitations.md, "Shared experts
 stay resident") get pinned slots after the class's LRU ranges and run in the
 same FFN launch as the routed experts (moe_route_shared widens the layer).
+A layer may route by biased or grouped scores (LayerSpec.route), and
+Streamer.block runs all of a layer around its routed experts: the residual
+sum and norm, the router, the experts, and an always-on expert of its own
+width in 8-bit integers (IntExpert).
 """
 from __future__ import annotations
 
@@ -32,6 +36,12 @@ class LayerSpec:
     bank: torch.Tensor            # pinned uint8 [rows, slot_bytes] of this layer's class
     bank_row: list                # expert e -> row of `bank`
     shared: torch.Tensor | None = None  # uint8 [n_shared, slot_bytes]: the layer's shared experts
+    route: ops.RouteConfig | None = None      # moe_route_grouped instead of moe_route
+    route_bias: torch.Tensor | None = None    # fp32 [E]: the bias of the choice (with route)
+    # what Streamer.block runs around the experts
+    norm: torch.Tensor | None = None          # bf16 [H]: the norm's gamma
+    router: torch.Tensor | None = None        # bf16 [E, H]
+    always: "IntExpert | None" = None         # an always-on expert next to the routed ones
 
 
 def quantize_bank_gpu(E: int, desc: ops.LayerDesc, seed: int, device="cuda", std: float = 0.02) -> torch.Tensor:
@@ -51,6 +61,51 @@ def quantize_bank_gpu(E: int, desc: ops.LayerDesc, seed: int, device="cuda", std
         ops.moe_quantize_rows(w_d, H, I, g, desc.bits_down, base + lay.down)
         bank[e].copy_(slot, non_blocking=False)
     return bank
+
+
+class IntExpert:
+    """An always-on SwiGLU expert of its own width I in 8-bit integers: gate
+    and up rows w_gu [2I, H] and down rows w_down [H, I] (fp32 or bf16, on the
+    device) are quantised once, on `stream` (later calls on another stream wait
+    for it themselves), with a scale per output; the activations take a scale
+    per token."""
+
+    def __init__(self, w_gu: torch.Tensor, w_down: torch.Tensor, max_tokens: int,
+                 stream: torch.cuda.Stream | None = None):
+        self.H, self.I = w_gu.shape[1], w_gu.shape[0] // 2
+        assert tuple(w_down.shape) == (self.H, self.I) and w_gu.shape[0] == 2 * self.I
+        dev = w_gu.device
+        self.max_tokens = max_tokens
+        st = stream or torch.cuda.current_stream(dev)
+
+        def quantize(w):
+            w = w.contiguous()
+            q = torch.empty(w.shape, dtype=torch.int8, device=dev)
+            s = torch.empty(w.shape[0], dtype=torch.float32, device=dev)
+            st.wait_stream(torch.cuda.current_stream(dev))  # w and the buffers come from there
+            ops.moe_quantize_channels(w, ops.MOE_F32 if w.dtype == torch.float32 else ops.MOE_BF16, w.shape[0],
+                                      w.shape[1], q, s, st)
+            w.record_stream(st)
+            return q, s
+
+        self.gu_q, self.gu_s = quantize(w_gu)
+        self.down_q, self.down_s = quantize(w_down)
+        self.gu = torch.empty((max_tokens, 2 * self.I), dtype=torch.bfloat16, device=dev)
+        self.hq = torch.empty((max_tokens, self.I), dtype=torch.int8, device=dev)
+        self.hs = torch.empty(max_tokens, dtype=torch.float32, device=dev)
+
+    LAUNCHES = 3
+
+    def add(self, xq, x_scale, T: int, y, dev_err, row_w=None, stream=None) -> None:
+        """y [T, H] (fp32) += row_w[t] (1 without) x the expert's output for
+        tokens given as codes and scales (moe_add_norm_quant)."""
+        if T > self.max_tokens:
+            raise ops.MoeError(ops.MOE_ERR_CAPACITY, "IntExpert.add")
+        ops.moe_int_matmul(xq, x_scale, T, self.gu_q, self.gu_s, 2 * self.I, self.H, None, None, self.gu,
+                           ops.MOE_BF16, dev_err, stream)
+        ops.moe_swiglu_quant(self.gu, ops.MOE_BF16, T, self.I, self.hq, self.hs, stream)
+        ops.moe_int_matmul(self.hq, self.hs, T, self.down_q, self.down_s, self.H, self.I, y, row_w, y, ops.MOE_F32,
+                           dev_err, stream)
 
 
 class Streamer:
@@ -138,7 +193,11 @@ class Streamer:
             self._ctx.append(ops.LayerCtx(C.pointer(spec.desc), self.pools[self.layer_class[l]].data_ptr(),
                                           self.class_n_slots[self.layer_class[l]],
                                           self.class_bytes[self.layer_class[l]], self.table_dev[l].data_ptr(),
-                                          self.table_pin[l].data_ptr(), rows, n_shared, None))
+                                          self.table_pin[l].data_ptr(), rows, n_shared, None,
+                                          C.pointer(spec.route) if spec.route is not None else None,
+                                          spec.route_bias.data_ptr() if spec.route_bias is not None else None))
+        # Streamer.block: the experts' input, its codes and the router's logits (allocated at the first call)
+        self.x = self.xq = self.x_scale = self.logits = None
         self.ffn_events = None     # list to collect (start, end) CUDA events around FFN calls
         # guessed prefetch (moe_decode_layer_ahead): its own copy stream, state and buffers
         self.prefetch = ops.Prefetch(self.n_layers)
@@ -215,8 +274,11 @@ class Streamer:
     # -- stages -------------------------------------------------------------
     def route_sort(self, layer: int, x, logits, T: int, L: float = 0.0, want_sorted_x: bool = False):
         d, dw = self.layers[layer].desc, self.wdesc[layer]
-        s = self.stream
-        if self.ns:
+        spec, s = self.layers[layer], self.stream
+        if spec.route is not None:
+            ops.moe_route_grouped(logits, T, d, spec.route, spec.route_bias, L, self.table_dev[layer], self.ns, None,
+                                  self.ids, self.w, s)
+        elif self.ns:
             ops.moe_route_shared(logits, T, d, L, self.table_dev[layer], self.ns, None, self.ids, self.w, s)
         else:
             ops.moe_route(logits, T, d, L, self.table_dev[layer], self.ids, self.w, s)
@@ -273,7 +335,7 @@ class Streamer:
     def _decode_launches(self, layer: int, T: int, full: bool, n_installed: int, guessing: bool = False) -> int:
         d = self.layers[layer].desc
         tc = self.uses_tc(layer, T)
-        if T == 1 and not tc:
+        if T == 1 and not tc and self.layers[layer].route is None:
             if not self.ns and full and not guessing and d.E <= 1024 and self._ffn_launches(layer, T, self.Ew) == 1:
                 return 1  # moe_route_expert_ffn: every stage in the FFN launch
             n = 1  # moe_route_sort_lookup
@@ -359,6 +421,41 @@ class Streamer:
                 s.synchronize()  # previous pass's FFN done before its slots can be reused
                 self._install_pass(layer, pe)
             self.ffn(layer, x, T, p, PASS_EXPERTS, y)
+        return y
+
+    def block(self, layer: int, h: torch.Tensor, delta, T: int, L: float = 0.0, eps: float = 1e-6, prefill=None,
+              row_w=None, y=None):
+        """One layer around its experts, on self.stream: h [T, H] (bf16 or fp32,
+        the residual stream) takes delta (fp32 or bf16 [T, H], the previous
+        block's output, or None) in place and is normed; the layer's router
+        scores the result; the routed experts run (prefill_layer, by default
+        above 64 tokens, else decode_layer) and the always-on expert, if the
+        layer has one, adds its output (times row_w [T] fp32).  Returns y fp32
+        [T, H], the next block's delta."""
+        spec, s = self.layers[layer], self.stream
+        if T < 1 or T > self.max_tokens:
+            raise ops.MoeError(ops.MOE_ERR_CAPACITY, "Streamer.block")
+        if self.x is None:
+            new = lambda *shape, dt: torch.empty(shape, dtype=dt, device=self.device)  # noqa: E731
+            self.x = new(self.max_tokens, self.H, dt=torch.bfloat16)
+            self.xq = new(self.max_tokens, self.H, dt=torch.int8)
+            self.x_scale = new(self.max_tokens, dt=torch.float32)
+            self.logits = new(self.max_tokens, self.E, dt=torch.float32)
+            s.wait_stream(torch.cuda.current_stream(self.device))  # the buffers' memory comes from there
+        kind = lambda t: ops.MOE_F32 if t.dtype == torch.float32 else ops.MOE_BF16  # noqa: E731
+        codes = spec.always is not None
+        ops.moe_add_norm_quant(h, kind(h), delta, ops.MOE_BF16 if delta is None else kind(delta), spec.norm, eps, T,
+                               self.H, h if delta is not None else None, self.x, self.xq if codes else None,
+                               self.x_scale if codes else None, s)
+        ops.moe_router_logits(self.x, T, spec.router, None, 1.0, self.E, self.H, self.logits, s)
+        self.launches += 2
+        if (T > 64) if prefill is None else prefill:
+            y = self.prefill_layer(layer, self.x, self.logits, T, y)
+        else:
+            y = self.decode_layer(layer, self.x, self.logits, T, L, y)
+        if codes:
+            spec.always.add(self.xq, self.x_scale, T, y, self.dev_err, row_w, s)
+            self.launches += spec.always.LAUNCHES
         return y
 
     def check_dev_err(self) -> int:
