@@ -596,8 +596,8 @@ typedef struct {
 } moe_layer_ctx;
 
 /* (A layer with `route` set takes moe_route_grouped where the calls below say
- * moe_route or moe_route_shared, and for one token the separate sort and
- * lookup; its guesses, too.) */
+ * moe_route or moe_route_shared, for its guesses, too; the FFN launch that
+ * routes its token itself is not for it.) */
 
 /* One decode layer, T <= 64 tokens (RFC "How the prototype works": each layer
  * copies its routing to the host once; misses cost one host-to-device copy

@@ -43,6 +43,42 @@ moe_status check_route_config(const moe_layer_desc* d, const moe_route_config* c
   return MOE_OK;
 }
 
+// The checks and kernel arguments of moe_route_grouped.
+moe_status route_grouped_args(const float* logits, int32_t T, const moe_layer_desc* d, const moe_route_config* c,
+                              const float* bias, float L, const int32_t* slot_table, int32_t n_shared,
+                              const float* shared_w, int32_t* ids, float* w, RouteGroupedArgs* a) {
+  moe_status s = check_desc(d);
+  if (s != MOE_OK) return s;
+  s = check_route_config(d, c);
+  if (s != MOE_OK) return s;
+  if (T < 0 || !(L >= 0.0f) || L > 1e30f || n_shared < 0 || n_shared > kMaxShared) return MOE_ERR_INVALID;
+  if (T == 0) return MOE_OK;
+  if (!logits || !ids || !w) return MOE_ERR_INVALID;
+  if (L > 0.0f && !slot_table) return MOE_ERR_INVALID;
+  if (!aligned(logits, 4) || !aligned(bias, 4) || !aligned(slot_table, 4) || !aligned(shared_w, 4) ||
+      !aligned(ids, 4) || !aligned(w, 4))
+    return MOE_ERR_INVALID;
+  if ((int64_t)T * d->k > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  a->logits = logits;
+  a->T = T;
+  a->E = d->E;
+  a->k = d->k;
+  a->G = c->n_groups;
+  a->top = c->top_groups;
+  a->gtop = c->group_top;
+  a->sigmoid = c->score == MOE_SCORE_SIGMOID;
+  a->renorm = c->renormalise != 0;
+  a->scale = c->scale;
+  a->bias = bias;
+  a->L = L;
+  a->table = slot_table;
+  a->ns = n_shared;
+  a->shared_w = shared_w;
+  a->ids = ids;
+  a->w = w;
+  return MOE_OK;
+}
+
 thread_local const char* g_last_cuda_error = "no error";
 
 std::atomic<long long> g_wait_limit{kDefaultWaitCycles};
@@ -408,39 +444,31 @@ moe_status moe_router_logits(const uint16_t* x, int32_t T, const uint16_t* W, co
   return cuda_status(launch_router(x, W, bias, scale, T, E, H, logits, stream));
 }
 
+// moe_route_grouped for one token, then its sort and slot lookup in the same
+// launch and, with host_meta, the active list in host memory: what
+// moe_internal_route_sort_lookup is to moe_route_shared.
+__attribute__((visibility("hidden"))) moe_status moe_internal_route_grouped_sort_lookup(
+    const float* logits, const moe_layer_desc* d, const moe_route_config* c, const float* bias, float L,
+    const int32_t* slot_table, int32_t n_shared, const float* shared_w, int32_t n_slots, int32_t* ids, float* w,
+    int32_t* offsets, int32_t* pairs, int32_t* active, int32_t* n_active, int32_t* slots, int32_t* miss,
+    int32_t* n_miss, int32_t* dev_err, cudaStream_t stream, int32_t* host_meta, int32_t seq) {
+  RouteGroupedArgs a{};
+  const moe_status s = route_grouped_args(logits, 1, d, c, bias, L, slot_table, n_shared, shared_w, ids, w, &a);
+  if (s != MOE_OK) return s;
+  if (d->k + n_shared > 32) return MOE_ERR_UNSUPPORTED;  // the widened layer, as moe_sort takes it
+  if (n_slots < 0 || !slot_table || !offsets || !pairs || !active || !n_active || !slots || !miss || !n_miss)
+    return MOE_ERR_INVALID;
+  const SortLookupArgs o{slot_table, n_slots, offsets, pairs, active, n_active, slots, miss, n_miss, dev_err,
+                         host_meta, seq};
+  return cuda_status(launch_route_grouped_sort_lookup(a, o, stream));
+}
+
 moe_status moe_route_grouped(const float* logits, int32_t T, const moe_layer_desc* d, const moe_route_config* c,
                              const float* bias, float L, const int32_t* slot_table, int32_t n_shared,
                              const float* shared_w, int32_t* ids, float* w, cudaStream_t stream) {
-  moe_status s = check_desc(d);
-  if (s != MOE_OK) return s;
-  s = check_route_config(d, c);
-  if (s != MOE_OK) return s;
-  if (T < 0 || !(L >= 0.0f) || L > 1e30f || n_shared < 0 || n_shared > kMaxShared) return MOE_ERR_INVALID;
-  if (T == 0) return MOE_OK;
-  if (!logits || !ids || !w) return MOE_ERR_INVALID;
-  if (L > 0.0f && !slot_table) return MOE_ERR_INVALID;
-  if (!aligned(logits, 4) || !aligned(bias, 4) || !aligned(slot_table, 4) || !aligned(shared_w, 4) ||
-      !aligned(ids, 4) || !aligned(w, 4))
-    return MOE_ERR_INVALID;
-  if ((int64_t)T * d->k > (1 << 24)) return MOE_ERR_UNSUPPORTED;
   RouteGroupedArgs a{};
-  a.logits = logits;
-  a.T = T;
-  a.E = d->E;
-  a.k = d->k;
-  a.G = c->n_groups;
-  a.top = c->top_groups;
-  a.gtop = c->group_top;
-  a.sigmoid = c->score == MOE_SCORE_SIGMOID;
-  a.renorm = c->renormalise != 0;
-  a.scale = c->scale;
-  a.bias = bias;
-  a.L = L;
-  a.table = slot_table;
-  a.ns = n_shared;
-  a.shared_w = shared_w;
-  a.ids = ids;
-  a.w = w;
+  const moe_status s = route_grouped_args(logits, T, d, c, bias, L, slot_table, n_shared, shared_w, ids, w, &a);
+  if (s != MOE_OK || T == 0) return s;
   return cuda_status(launch_route_grouped(a, device_sms(), stream));
 }
 

@@ -46,6 +46,12 @@ extern "C" moe_status moe_internal_route_sort_lookup(
     int32_t* active, int32_t* n_active, int32_t* slots, int32_t* miss, int32_t* n_miss, int32_t* dev_err,
     cudaStream_t stream, int32_t* host_meta, int32_t seq);
 
+extern "C" moe_status moe_internal_route_grouped_sort_lookup(
+    const float* logits, const moe_layer_desc* d, const moe_route_config* c, const float* bias, float L,
+    const int32_t* slot_table, int32_t n_shared, const float* shared_w, int32_t n_slots, int32_t* ids, float* w,
+    int32_t* offsets, int32_t* pairs, int32_t* active, int32_t* n_active, int32_t* slots, int32_t* miss,
+    int32_t* n_miss, int32_t* dev_err, cudaStream_t stream, int32_t* host_meta, int32_t seq);
+
 struct moe_prefetch {
   struct Batch {
     cudaEvent_t ev;
@@ -219,9 +225,9 @@ moe_status decode_layer(moe_cache* cache, int32_t layer, const moe_layer_ctx* lc
   // experts always), it reads x sorted by expert
   uint16_t* xs =
       (b->x_sorted && moe_ffn_kernel_path(d, T, 1) == MOE_PATH_TC_PREFILL) ? b->x_sorted : nullptr;
-  // one token without sorted x: routing (moe_route's), sort and lookup in one launch
-  const bool one = T == 1 && !xs && !lc->route;
-  if (one && ns == 0 && !(G && G->n > 0) && moe_cache_resident(cache, layer) >= E0) {
+  // one token without sorted x: routing, sort and lookup in one launch
+  const bool one = T == 1 && !xs;
+  if (one && !lc->route && ns == 0 && !(G && G->n > 0) && moe_cache_resident(cache, layer) >= E0) {
     // a fully resident layer: the FFN launch routes the token itself (the host needs none of it)
     const moe_status r = moe_route_expert_ffn(x, logits, T, d0, L, lc->pool, lc->n_slots, lc->table_dev, b->ids,
                                               b->w, b->offsets, b->pairs, active, n_active, b->slots, miss, n_miss,
@@ -239,7 +245,12 @@ moe_status decode_layer(moe_cache* cache, int32_t layer, const moe_layer_ctx* lc
     host_meta = b->meta_host;
     seq = next_host_seq();
   }
-  if (one) {
+  if (one && lc->route) {
+    s = moe_internal_route_grouped_sort_lookup(logits, d0, lc->route, lc->route_bias, L, lc->table_dev, ns,
+                                               lc->shared_w, lc->n_slots, b->ids, b->w, b->offsets, b->pairs, active,
+                                               n_active, b->slots, miss, n_miss, b->dev_err, stream, host_meta, seq);
+    if (s != MOE_OK) return s;
+  } else if (one) {
     s = moe_internal_route_sort_lookup(logits, T, d0, L, lc->table_dev, ns, lc->shared_w, lc->n_slots, b->ids,
                                        b->w, b->offsets, b->pairs, active, n_active, b->slots, miss, n_miss,
                                        b->dev_err, stream, host_meta, seq);

@@ -70,6 +70,15 @@ struct FfnArgs {
 // experts a layer may have for the fused decode kernel to route its token itself
 constexpr int kRouteMaxExperts = 1024;
 
+// the sort and lookup outputs of one token (route_tail.cuh)
+struct SortLookupArgs {
+  const int32_t* table;
+  int n_slots;
+  int32_t *offsets, *pairs, *active, *n_active, *slots, *miss, *n_miss, *dev_err;
+  int32_t* host_meta;
+  int32_t seq;
+};
+
 // moe_route_grouped
 struct RouteGroupedArgs {
   const float* logits;
@@ -158,6 +167,8 @@ cudaError_t launch_quantize(const float* w, int rows, int K, int g, int b, int g
 cudaError_t launch_dequant_slot(const uint8_t* slot, const moe_layer_desc& d, const Layout& L, float* out32,
                                 uint16_t* out16, cudaStream_t st);
 cudaError_t launch_route_grouped(const RouteGroupedArgs& a, int num_sms, cudaStream_t st);
+// one token (a.T == 1): routing, sort and lookup in one launch
+cudaError_t launch_route_grouped_sort_lookup(const RouteGroupedArgs& a, const SortLookupArgs& o, cudaStream_t st);
 cudaError_t launch_row_quant(const RowQuantArgs& a, int op, bool in_f32, bool delta_f32, cudaStream_t st);
 cudaError_t launch_int_matmul(const IntMatmulArgs& a, int num_sms, cudaStream_t st);
 bool ffn_decode_supported(const moe_layer_desc& d);

@@ -28,6 +28,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "route_tail.cuh"
 
 namespace moe {
 namespace {
@@ -64,12 +65,12 @@ __device__ __forceinline__ float warp_min(float v) { return unordered(__reduce_m
 
 __device__ __forceinline__ float exp2_of(float x) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ float rcp(float x) {
   float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -253,8 +254,10 @@ __device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const floa
 #pragma unroll
     for (int i = 0; i < NPL; ++i) key[i] = have(i) ? row[expert(i)] : -INFINITY;
   }
+  if (a.bias) {
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) bias[i] = a.bias && have(i) ? a.bias[expert(i)] : 0.0f;
+    for (int i = 0; i < NPL; ++i) bias[i] = have(i) ? a.bias[expert(i)] : 0.0f;
+  }
   if (lifted) {
 #pragma unroll
     for (int i = 0; i < NPL; ++i) resident |= (have(i) && a.table[expert(i)] >= 0 ? 1u : 0u) << i;
@@ -307,8 +310,10 @@ __device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const floa
       for (int i = 0; i < NPL; ++i) s[i] = __fmul_rn(s[i], inv);
       unit = (a.bias ? 36.0f : 8.0f) * 0x1p-24f * inv;
     }
+    if (a.bias) {  // c, before the lift
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) s[i] = __fadd_rn(s[i], bias[i]);  // c, before the lift
+      for (int i = 0; i < NPL; ++i) s[i] = __fadd_rn(s[i], bias[i]);
+    }
 #pragma unroll
     for (int i = 0; i < NPL; i += 2) {
       hi = max3(hi, have(i) ? s[i] : -INFINITY, have(i + 1) ? s[i + 1] : -INFINITY);
@@ -413,7 +418,7 @@ __device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const floa
     if (by_l) return l;
     float c = term(l);
     if (!a.sigmoid) c = __fmul_rn(c, inv);
-    c = __fadd_rn(c, a.bias ? a.bias[e] : 0.0f);
+    if (a.bias) c = __fadd_rn(c, a.bias[e]);
     return lifted && a.table[e] >= 0 ? __fadd_rn(c, lift) : c;
   };
   if (cnt <= 32) {
@@ -486,7 +491,7 @@ __device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const floa
     for (int e = lane; e < E; e += 32) {
       float c = term(row[e]);
       if (!a.sigmoid) c = __fmul_rn(c, inv);
-      c = __fadd_rn(c, a.bias ? a.bias[e] : 0.0f);
+      if (a.bias) c = __fadd_rn(c, a.bias[e]);
       if (c > hi - 2.0f * D) top64 = fmax(top64, exact(e));
       if (c < lo + 2.0f * D) low64 = fmax(low64, -exact(e));
     }
@@ -512,16 +517,11 @@ __device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const floa
   return true;
 }
 
+// One token by one warp; sm: warp_bytes(E) of shared memory.
 template <int NPL, bool FULL>
-__global__ void __launch_bounds__(256) route_grouped_kernel(const __grid_constant__ RouteGroupedArgs a) {
-  extern __shared__ __align__(16) char route_smem[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x * (blockDim.x >> 5) + warp;
-  pdl_wait();
-  pdl_launch_dependents();
-  if (t >= a.T) return;
+__device__ __forceinline__ void route_token(const RouteGroupedArgs& a, int t, char* sm) {
+  const int lane = threadIdx.x & 31;
   const float* row = a.logits + (size_t)t * a.E;
-  char* sm = route_smem + warp * warp_bytes(a.E);
   int my_e = 0;
   float w = 0.0f, M = 0.0f, sum = 0.0f;
   if (route_fast<NPL, FULL>(a, row, sm, my_e, M, sum)) {
@@ -549,25 +549,55 @@ __global__ void __launch_bounds__(256) route_grouped_kernel(const __grid_constan
   }
 }
 
+template <int NPL, bool FULL>
+__global__ void __launch_bounds__(256) route_grouped_kernel(const __grid_constant__ RouteGroupedArgs a) {
+  extern __shared__ __align__(16) char route_smem[];
+  const int warp = threadIdx.x >> 5, t = blockIdx.x * (blockDim.x >> 5) + warp;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (t < a.T) route_token<NPL, FULL>(a, t, route_smem + warp * warp_bytes(a.E));
+}
+
+// One decode token: its routing by warp 0, then the sort and the slot lookup
+// of its experts by the block, as moe_sort and moe_slot_lookup write them.
+template <int NPL, bool FULL>
+__global__ void __launch_bounds__(256)
+    route_grouped_sort_lookup_kernel(const __grid_constant__ RouteGroupedArgs a, const SortLookupArgs o) {
+  extern __shared__ __align__(16) char route_smem[];
+  pdl_wait();
+  pdl_launch_dependents();
+  if (threadIdx.x < 32) route_token<NPL, FULL>(a, 0, route_smem);
+  sort_lookup_token(a.ids, a.k + a.ns, a.E + a.ns, o);
+}
+
 template <int NPL>
-const void* route_kernel_of(const RouteGroupedArgs& a) {
-  const bool full = a.E == 32 * NPL && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0;
-  return full ? reinterpret_cast<const void*>(route_grouped_kernel<NPL, true>)
+const void* route_kernel_of(const RouteGroupedArgs& a, bool sort) {
+  if (a.E == 32 * NPL && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0)
+    return sort ? reinterpret_cast<const void*>(route_grouped_sort_lookup_kernel<NPL, true>)
+                : reinterpret_cast<const void*>(route_grouped_kernel<NPL, true>);
+  return sort ? reinterpret_cast<const void*>(route_grouped_sort_lookup_kernel<NPL, false>)
               : reinterpret_cast<const void*>(route_grouped_kernel<NPL, false>);
+}
+
+const void* route_kernel_of(const RouteGroupedArgs& a, bool sort) {
+  return a.E <= 128   ? route_kernel_of<4>(a, sort)
+         : a.E <= 256 ? route_kernel_of<8>(a, sort)
+         : a.E <= 512 ? route_kernel_of<16>(a, sort)
+                      : route_kernel_of<32>(a, sort);
 }
 
 }  // namespace
 
 cudaError_t launch_route_grouped(const RouteGroupedArgs& a, int num_sms, cudaStream_t st) {
-  const void* kern = a.E <= 128   ? route_kernel_of<4>(a)
-                     : a.E <= 256 ? route_kernel_of<8>(a)
-                     : a.E <= 512 ? route_kernel_of<16>(a)
-                                  : route_kernel_of<32>(a);
   // few tokens spread over the SMs; no more than 48 KB of shared memory a block
   int warps = a.T / num_sms;
   warps = warps < 1 ? 1 : warps > 8 ? 8 : warps;
   while (warps > 1 && warps * warp_bytes(a.E) > 48 * 1024) --warps;
-  return launch_pdl(kern, (a.T + warps - 1) / warps, 32 * warps, warps * warp_bytes(a.E), st, a);
+  return launch_pdl(route_kernel_of(a, false), (a.T + warps - 1) / warps, 32 * warps, warps * warp_bytes(a.E), st, a);
+}
+
+cudaError_t launch_route_grouped_sort_lookup(const RouteGroupedArgs& a, const SortLookupArgs& o, cudaStream_t st) {
+  return launch_pdl(route_kernel_of(a, true), 1, 256, warp_bytes(a.E), st, a, o);
 }
 
 }  // namespace moe

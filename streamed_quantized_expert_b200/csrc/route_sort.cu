@@ -12,6 +12,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "route_block.cuh"
+#include "route_tail.cuh"
 
 namespace moe {
 
@@ -126,14 +127,7 @@ __global__ void __launch_bounds__(256) route_select_kernel(const float* __restri
 
 // One decode token's stages 1-3 in one block: route (as route_select_kernel,
 // with ns shared experts E .. E + ns - 1 of weight sw after the top k), then
-// the sort of its k + ns pairs (distinct experts: the active list is the
-// routed experts ascending, then the shared ones; pair j of rank r sits at
-// position r) and the slot lookup over the whole active list (as
-// sort_small_kernel and lookup_kernel write them for T = 1).  With host_meta
-// (page-locked host memory the device can address), warp 1 also writes
-// n_active to host_meta[0] and the active list to host_meta[2 ..], then, once
-// those writes are visible system-wide, seq to host_meta[1]: the host waits
-// for seq there instead of copying the list back and synchronising.
+// the sort and the slot lookup of its experts (sort_lookup_token).
 template <int NPT>
 __global__ void __launch_bounds__(256) route_sort_lookup_kernel(
     const float* __restrict__ logits, int E, int k, float L, const int32_t* __restrict__ table, int ns,
@@ -141,49 +135,11 @@ __global__ void __launch_bounds__(256) route_sort_lookup_kernel(
     int32_t* __restrict__ offsets, int32_t* __restrict__ pairs, int32_t* __restrict__ active,
     int32_t* __restrict__ n_active, int32_t* __restrict__ slots, int32_t* __restrict__ miss,
     int32_t* __restrict__ n_miss, int32_t* __restrict__ dev_err, int32_t* host_meta, int32_t seq) {
-  __shared__ int s_sel[32];  // the token's experts, rank order (k + ns <= 32)
-  __shared__ int s_act[32];  // ascending
-  const int tid = threadIdx.x, n = k + ns, Ew = E + ns;
   pdl_wait();
   pdl_launch_dependents();
   route_select_token<NPT>(logits, E, k, L, table, ids, w, ns, (ns > 0 && sw) ? sw[0] : 1.0f);
-  __syncthreads();  // the block's own global writes of ids are visible to it
-  if (tid < n) s_sel[tid] = ids[tid];
-  __syncthreads();
-  if (tid < n) {
-    const int e = s_sel[tid];
-    int r = 0;
-    for (int j = 0; j < n; ++j) r += s_sel[j] < e;
-    s_act[r] = e;
-    active[r] = e;
-    pairs[r] = tid;
-  }
-  for (int e = tid; e <= Ew; e += 256) {
-    int c = 0;
-    for (int j = 0; j < n; ++j) c += s_sel[j] < e;
-    offsets[e] = c;
-  }
-  __syncthreads();
-  if (tid < 32) {  // lookup: one lane per active expert (k + ns <= 32)
-    const bool in = tid < n;
-    const int e = in ? s_act[tid] : -1;
-    const int sl = in ? table[e] : 0;
-    if (in) slots[tid] = sl;
-    if (in && sl >= n_slots && dev_err) atomicOr(dev_err, MOE_DEV_ERR_SLOT_RANGE);
-    const unsigned bal = __ballot_sync(0xffffffffu, in && sl < 0);
-    if (in && sl < 0) miss[__popc(bal & ((1u << tid) - 1u))] = e;
-    if (tid == 0) {
-      *n_active = n;
-      *n_miss = __popc(bal);
-    }
-  } else if (tid < 64 && host_meta) {
-    const int lane = tid - 32;
-    if (lane < n) host_meta[2 + lane] = s_act[lane];
-    if (lane == 0) host_meta[0] = n;
-    __threadfence_system();
-    __syncwarp();
-    if (lane == 0) *reinterpret_cast<volatile int32_t*>(host_meta + 1) = seq;
-  }
+  sort_lookup_token(ids, k + ns, E + ns,
+                    {table, n_slots, offsets, pairs, active, n_active, slots, miss, n_miss, dev_err, host_meta, seq});
 }
 
 // ---------------------------------------------------------------------------

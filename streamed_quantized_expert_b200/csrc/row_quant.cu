@@ -90,7 +90,7 @@ __device__ __forceinline__ float warp_max(float m) {
 
 __device__ __forceinline__ float rcp(float x) {
   float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -199,7 +199,7 @@ __device__ __forceinline__ float scale_of(float amax, float r) {
 
 __device__ __forceinline__ float exp2_of(float x) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -212,17 +212,17 @@ __device__ __forceinline__ float exp2_of(float x) {
 // instruction; 50 us one by one).
 __device__ __forceinline__ F2 swiglu_of(F2 g2, F2 u) {
   const float2 g = split2(g2);
-  const F2 m = pack2(fminf(fabsf(g.x), 128.0f), fminf(fabsf(g.y), 128.0f)), minus = pack2(-1.0f, -1.0f);
-  const F2 hi = pack2(-0x1.715476p+0f, -0x1.715476p+0f), lo = pack2(-0x1.4ae0cp-26f, -0x1.4ae0cp-26f);
-  const F2 t = mul2(m, hi), e = fma2(m, lo, fma2(m, hi, mul2(t, minus)));
+  const F2 m = pack2(fminf(fabsf(g.x), 128.0f), fminf(fabsf(g.y), 128.0f)), one = pack2(1.0f, 1.0f);
+  const F2 t = mul2(m, pack2(0x1.715476p+0f, 0x1.715476p+0f));  // -t above
+  const F2 e = fma2(m, pack2(-0x1.4ae0cp-26f, -0x1.4ae0cp-26f), fma2(m, pack2(-0x1.715476p+0f, -0x1.715476p+0f), t));
   const float2 tf = split2(t);
-  const F2 p = pack2(exp2_of(tf.x), exp2_of(tf.y));
-  const F2 s2 = fma2(mul2(e, pack2(0x1.62e43p-1f, 0x1.62e43p-1f)), p, p);
-  const F2 nd = fma2(s2, minus, minus);  // -(1 + s)
-  const float2 s = split2(s2), df = split2(mul2(nd, minus));
-  const F2 n = mul2(g2, pack2(g.x < 0.0f ? s.x : 1.0f, g.y < 0.0f ? s.y : 1.0f));
-  const F2 r = pack2(rcp(df.x), rcp(df.y)), q = mul2(n, r);
-  return mul2(fma2(fma2(nd, q, n), r, q), u);
+  const F2 p = pack2(exp2_of(-tf.x), exp2_of(-tf.y));
+  const F2 s2 = fma2(mul2(e, pack2(0x1.62e43p-1f, 0x1.62e43p-1f)), p, p), d2 = add2(s2, one);
+  const float2 s = split2(s2), d = split2(d2);
+  // with n = -g (1 or s) and r = -1 / (1 + s) rounded: q = n r, then q + (q (1 + s) + n) r
+  const F2 n = mul2(g2, pack2(g.x < 0.0f ? -s.x : -1.0f, g.y < 0.0f ? -s.y : -1.0f));
+  const F2 r = pack2(rcp(-d.x), rcp(-d.y)), q = mul2(n, r);
+  return mul2(fma2(fma2(d2, q, n), r, q), u);
 }
 
 // What a thread reads for eight columns of a row: one or two arrays of eight values.
@@ -335,7 +335,7 @@ __device__ __forceinline__ float row_factor(const RowQuantArgs& a, float sum) {
 // Rows held in registers, CH pieces of eight columns a thread: one pass over
 // the data.  A row is a warp's (WARP: eight rows to a block) or a block's.
 template <int OP, bool HF32, bool DF32, int CH, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : CH == 4 ? 512 : 1024) row_quant_kernel(const RowQuantArgs a) {
+__global__ void __launch_bounds__(WARP ? 256 : CH == 4 ? 512 : 1024, CH == 4 ? 2 : 1) row_quant_kernel(const RowQuantArgs a) {
   using Raw = RowRaw<OP, HF32, DF32>;
   const int n = WARP ? 32 : blockDim.x, i = WARP ? threadIdx.x & 31 : threadIdx.x;
   const int64_t row = WARP ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;

@@ -179,19 +179,11 @@ def _ck(status: int, where: str) -> None:
 
 def _ptr(t) -> int | None:
     """Device (or host) address of a tensor / int / None."""
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or t.__class__ is int else t.data_ptr()
 
 
 def _stream(s) -> int | None:
-    if s is None:
-        return None
-    if isinstance(s, int):
-        return s
-    return s.cuda_stream  # torch.cuda.Stream
+    return s if s is None or s.__class__ is int else s.cuda_stream  # torch.cuda.Stream
 
 
 def desc(E, k, H, I, group, bits_gu, bits_down=None) -> LayerDesc:
