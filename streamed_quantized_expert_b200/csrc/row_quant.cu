@@ -457,7 +457,7 @@ cudaError_t launch_row_quant(const RowQuantArgs& a, int op, bool in_f32, bool de
   const RowPlan k = op == kRowNorm     ? row_plan<kRowNorm>(a.H, in_f32, delta_f32)
                     : op == kRowSwiglu ? row_plan<kRowSwiglu>(a.H, in_f32, false)
                                        : row_plan<kRowPlain>(a.H, in_f32, false);
-  return launch_pdl(k.fn, (a.T + k.rows - 1) / k.rows, k.threads, 0, st, a);
+  return launch_pdl(k.fn, (int)(((int64_t)a.T + k.rows - 1) / k.rows), k.threads, 0, st, a);
 }
 
 }  // namespace moe

@@ -27,6 +27,13 @@ import torch
 
 from . import ops
 
+def _kind(t: torch.Tensor) -> int:
+    """The library's type of a tensor (bf16 also as 16-bit patterns)."""
+    if t.dtype not in (torch.float32, torch.bfloat16, torch.int16, torch.uint16) or not t.is_contiguous():
+        raise ops.MoeError(ops.MOE_ERR_INVALID, f"a dense fp32 or bf16 tensor, got {t.dtype}")
+    return ops.MOE_F32 if t.dtype == torch.float32 else ops.MOE_BF16
+
+
 PASS_EXPERTS = 64  # RFC / PR #50717: sorted prefill runs 64 experts at a time
 
 
@@ -83,8 +90,7 @@ class IntExpert:
             q = torch.empty(w.shape, dtype=torch.int8, device=dev)
             s = torch.empty(w.shape[0], dtype=torch.float32, device=dev)
             st.wait_stream(torch.cuda.current_stream(dev))  # w and the buffers come from there
-            ops.moe_quantize_channels(w, ops.MOE_F32 if w.dtype == torch.float32 else ops.MOE_BF16, w.shape[0],
-                                      w.shape[1], q, s, st)
+            ops.moe_quantize_channels(w, _kind(w), w.shape[0], w.shape[1], q, s, st)
             w.record_stream(st)
             return q, s
 
@@ -435,6 +441,8 @@ class Streamer:
         spec, s = self.layers[layer], self.stream
         if T < 1 or T > self.max_tokens:
             raise ops.MoeError(ops.MOE_ERR_CAPACITY, "Streamer.block")
+        if spec.norm is None or spec.router is None or any(t is not None and t.numel() < T * self.H for t in (h, delta)):
+            raise ops.MoeError(ops.MOE_ERR_INVALID, "Streamer.block")
         if self.x is None:
             new = lambda *shape, dt: torch.empty(shape, dtype=dt, device=self.device)  # noqa: E731
             self.x = new(self.max_tokens, self.H, dt=torch.bfloat16)
@@ -442,9 +450,8 @@ class Streamer:
             self.x_scale = new(self.max_tokens, dt=torch.float32)
             self.logits = new(self.max_tokens, self.E, dt=torch.float32)
             s.wait_stream(torch.cuda.current_stream(self.device))  # the buffers' memory comes from there
-        kind = lambda t: ops.MOE_F32 if t.dtype == torch.float32 else ops.MOE_BF16  # noqa: E731
         codes = spec.always is not None
-        ops.moe_add_norm_quant(h, kind(h), delta, ops.MOE_BF16 if delta is None else kind(delta), spec.norm, eps, T,
+        ops.moe_add_norm_quant(h, _kind(h), delta, ops.MOE_BF16 if delta is None else _kind(delta), spec.norm, eps, T,
                                self.H, h if delta is not None else None, self.x, self.xq if codes else None,
                                self.x_scale if codes else None, s)
         ops.moe_router_logits(self.x, T, spec.router, None, 1.0, self.E, self.H, self.logits, s)

@@ -147,3 +147,32 @@ def test_pointers_into_larger_buffers():
         assert (h[0] == 77).all() and (h[T + 1] == 77).all()
         h = h[1:T + 1]
         check(h if f32 else bf16_bits_to_f32(np.ascontiguousarray(h).view(np.uint16)), *a, f32)
+
+
+@pytest.mark.parametrize("T,N,K", [
+    (40, 9602, 1040), (100, 2306, 1040), (41, 2309, 2064), (250, 300, 4112),       # 64-token tiles; K whole, in 2, 4 and 8
+    (100, 9602, 1040), (513, 4099, 1040), (129, 19000, 2064), (700, 7001, 4112),  # 128 and 256 tokens, pairs of SMs
+    (1025, 4102, 2064)])
+def test_every_tile(T, N, K):
+    """Sizes at which each tile and split is chosen, with every kind of output
+    (even and odd N: paired and single bf16 stores)."""
+    for add, row_w, f32, in_place in ((False, False, False, False), (True, True, True, True), (True, False, False, False)):
+        a = inputs(T + N, T, N, K, add, row_w, extreme=True)
+        check(run(*a, f32, in_place), *a, f32)
+
+
+@pytest.mark.parametrize("T,N,K", [(129, 19000, 2064), (40, 2306, 2064)])
+def test_two_calls_at_once(T, N, K):
+    """The tiles that fill an SM's shared memory and tensor memory, on two streams."""
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    sets = [inputs(s, T, N, K, False, False) for s in range(2)]
+    bufs = [[dev(x) for x in a[:4]] + [torch.zeros((T, N), device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")]
+            for a in sets]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for st, b in zip(streams, bufs):
+            ops.moe_int_matmul(b[0], b[1], T, b[2], b[3], N, K, None, None, b[4], ops.MOE_F32, b[5], st)
+    torch.cuda.synchronize()
+    for a, b in zip(sets, bufs):
+        check(b[4].cpu().numpy(), *a, True)
+        assert int(b[5].item()) == 0

@@ -201,6 +201,10 @@ def test_block_refuses_too_many_tokens(orc):
         with pytest.raises(ops.MoeError) as ei:
             st.block(0, h, None, T)
         assert ei.value.status == ops.MOE_ERR_CAPACITY
+    for bad in (h.to(torch.float16), h.t(), h[:2]):  # a type the library lacks, not dense, too few rows
+        with pytest.raises(ops.MoeError) as ei:
+            st.block(0, bad, None, 3)
+        assert ei.value.status == ops.MOE_ERR_INVALID
     with pytest.raises(ops.MoeError) as ei:
         st.layers[0].always.add(h, h, 257, h, None)
     assert ei.value.status == ops.MOE_ERR_CAPACITY
