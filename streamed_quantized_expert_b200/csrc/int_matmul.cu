@@ -5,10 +5,14 @@
 // accumulation is exact in any order and any split of K gives the same bits;
 // the scales are applied once to each sum.
 //
-// Up to 16 tokens the weight bytes bound the call: im_rows_kernel streams
-// them through mma.sync, one block per 16 outputs.  Above, im_tc_kernel runs
-// on tcgen05 (kind::i8, s32 accumulators in TMEM) fed by TMA, with the weight
-// rows as the MMA's 128-row side so that a few dozen tokens fill its other side.
+// Up to 16 tokens (32 of few weights) the weight bytes bound the call:
+// im_rows_kernel streams them through mma.sync, one block per 16 outputs (1 x
+// 4096 x 8192 with fp32 sums: 7.5 us, 4.5 TB/s with the launch in it).  Above,
+// im_tc_kernel runs on tcgen05 (kind::i8, s32 accumulators in TMEM) fed by
+// TMA, with the weight rows as the MMA's 128-row side so that a few dozen
+// tokens fill its other side (48 x 5003 x 2048: 7.0 us), and im_pair_kernel
+// with two CTAs to a tile where chunks are long (4096 x 8192 x 4096: 90 us, 3.0
+// POP/s; 106 us over seconds, when the card's power limit lowers its clock).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
@@ -41,9 +45,13 @@ __device__ __forceinline__ void im_store(const IntMatmulArgs& a, int t, int n, f
 // ---------------------------------------------------------------------------
 // few tokens
 // ---------------------------------------------------------------------------
-constexpr int kRowsTokens = 16;  // tokens the streaming kernel takes
+// Tokens the streaming kernel takes, and takes where the weights are few: 24
+// tokens x 2048 x 768 run in 3.1 us here and 3.9 on the tensor-core tiles, x
+// 4096 x 2048 in 5.3 and 5.9, x 4096 x 8192 in 10.8 and 10.3.
+constexpr int kRowsTokens = 16, kRowsMaxTokens = 32;
+constexpr int64_t kRowsMaxWeights = 1 << 23;
 // 128-input units a warp keeps in flight; the registers hold fewer next to two token tiles
-__host__ __device__ constexpr int rows_depth(int nt) { return nt == 1 ? 4 : 2; }
+__host__ __device__ constexpr int rows_depth(int nt) { return nt == 1 ? 4 : nt == 2 ? 2 : 1; }
 
 // D (16 x 8, s32) += A (16 x 32, s8, row) . B (32 x 8, s8, column).
 __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -840,10 +848,14 @@ const void* rows_kernel(int W) {
 }  // namespace
 
 cudaError_t launch_int_matmul(const IntMatmulArgs& a, int num_sms, cudaStream_t st) {
-  if (a.T <= kRowsTokens) {
+  if (a.T <= kRowsTokens || (a.T <= kRowsMaxTokens && (int64_t)a.N * a.K <= kRowsMaxWeights)) {
     // enough units for each warp to fill its ring
     const int W = a.K >= 4096 ? 8 : a.K >= 2048 ? 4 : 2;
-    return launch_pdl(a.T <= 8 ? rows_kernel<1>(W) : rows_kernel<2>(W), (a.N + 15) / 16, 32 * W, 0, st, a);
+    const void* kern = a.T <= 8    ? rows_kernel<1>(W)
+                       : a.T <= 16 ? rows_kernel<2>(W)
+                       : a.T <= 24 ? rows_kernel<3>(W)
+                                   : rows_kernel<4>(W);
+    return launch_pdl(kern, (a.N + 15) / 16, 32 * W, 0, st, a);
   }
   const TcPlan p = tc_plan(a, num_sms);
   if (p.nb == 32) return launch_tc<32>(a, p.split, num_sms, st);

@@ -388,18 +388,17 @@ __device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const floa
       }
     }
   }
-  // threshold: the lanes' maxima, sorted descending
+  // threshold: of the lanes' maxima, the largest that is left after k have
+  // been taken away (equal ones together: then it is lower, which does no harm)
   float top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < NPL; i += 2) top = max3(top, key[i], key[i + 1]);
-#pragma unroll
-  for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-    for (int j = size >> 1; j; j >>= 1) {
-      const float o = __shfl_xor_sync(kAll, top, j);
-      top = ((lane & size) == 0 || size == 32) == ((lane & j) == 0) ? fmaxf(top, o) : fminf(top, o);
-    }
-  const float tau = k < 32 ? fmaxf(__shfl_sync(kAll, top, k), -FLT_MAX) : -FLT_MAX;
+  uint32_t rest = ordered(top), most_left = 0u;
+  for (int j = 0; j <= k; ++j) {
+    most_left = __reduce_max_sync(kAll, rest);
+    if (rest == most_left) rest = 0u;
+  }
+  const float tau = most_left > ordered(-FLT_MAX) ? unordered(most_left) : -FLT_MAX;
   uint32_t in = 0;
 #pragma unroll
   for (int i = 0; i < NPL; ++i) in |= (key[i] >= tau ? 1u : 0u) << i;
