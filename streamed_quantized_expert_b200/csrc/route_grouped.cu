@@ -18,11 +18,12 @@
 // maxima has at least k + 1 experts at or above it, and few more; those are
 // ranked by counting.
 //
-// What bounds it: instructions, some 700 a token of 512 experts (its 2 KB would
-// take 0.3 ns at 6.6 TB/s).  16384 tokens x 512 experts, softmax, k 10: 16.4 us;
-// 4096 x 256, sigmoid with bias and 4 of 8 groups, k 8: 8.5 us; one token of 512
-// with all of it: 4.5 us (243, 53 and 41 us where every score and choice is made
-// in 64 bits with a search of all experts per rank).
+// What bounds it: instructions, 545 a token of 512 experts (its 2 KB would take
+// 0.3 ns at 6.6 TB/s), and for a few thousand tokens their latency.  16384
+// tokens x 512 experts, softmax, k 10: 13.0 us; 4096 x 256, sigmoid with bias
+// and 4 of 8 groups, k 8: 8.2-8.9 us; one token of 512 with all of it: 4.3 us
+// (243, 53 and 41 us where every score and choice is made in 64 bits with a
+// search of all experts per rank).
 #include <cfloat>
 #include <climits>
 
@@ -229,12 +230,15 @@ __device__ __forceinline__ float max_abs3(float m, float a, float b) {  // NaN i
 // The token's choice in fp32, or of the candidates that fp32 leaves in 64
 // bits; false where that does not settle it.  my_e: lane j's expert (rank j);
 // M, sum: the softmax's exponent offset and denominator.  FULL: E = 32 NPL,
-// and the lanes hold four experts side by side.
-template <int NPL, bool FULL>
+// and the lanes hold four experts side by side.  PLAIN: no bias, substitution
+// or groups (code and registers of their own: 16384 x 512 takes 13.0 us, 16.1
+// with all of it in one kernel).
+template <int NPL, bool FULL, bool PLAIN>
 __device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const float* row, char* sm, int& my_e, float& M,
                                            float& sum) {
   const int lane = threadIdx.x & 31, E = a.E, k = a.k;
-  const bool lifted = a.L > 0.0f && a.table, by_l = !a.bias && !lifted, groups = a.top < a.G;
+  const bool lifted = !PLAIN && a.L > 0.0f && a.table, by_l = PLAIN || (!a.bias && !lifted);
+  const bool groups = !PLAIN && a.top < a.G;
   float* const sc = reinterpret_cast<float*>(sm);
   Cand* const wide = reinterpret_cast<Cand*>(sm);
   float* const skey = reinterpret_cast<float*>(sm + c_bytes(E));
@@ -254,7 +258,7 @@ __device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const floa
 #pragma unroll
     for (int i = 0; i < NPL; ++i) key[i] = have(i) ? row[expert(i)] : -INFINITY;
   }
-  if (a.bias) {
+  if (!PLAIN && a.bias) {
 #pragma unroll
     for (int i = 0; i < NPL; ++i) bias[i] = have(i) ? a.bias[expert(i)] : 0.0f;
   }
@@ -423,8 +427,13 @@ __device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const floa
   if (cnt <= 32) {
     const int e = lane < cnt ? cand[lane] : INT_MAX;
     const float c = lane < cnt ? choice(e) + 0.0f : -INFINITY;  // -0 as +0
-    int r = 0;
-    for (int j = 0; j < cnt; ++j) r += __shfl_sync(kAll, c, j) > c ? 1 : 0;
+    int r = 0;  // lanes without a candidate hold -inf and come before none
+#pragma unroll
+    for (int j = 0; j < 16; ++j) r += __shfl_sync(kAll, c, j) > c ? 1 : 0;
+    if (cnt > 16) {
+#pragma unroll
+      for (int j = 16; j < 32; ++j) r += __shfl_sync(kAll, c, j) > c ? 1 : 0;
+    }
     const uint32_t alike = __match_any_sync(kAll, __float_as_uint(c));
     if (__any_sync(kAll, lane < cnt && alike != (1u << lane)))
       for (int j = 0; j < cnt; ++j) {
@@ -517,13 +526,13 @@ __device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const floa
 }
 
 // One token by one warp; sm: warp_bytes(E) of shared memory.
-template <int NPL, bool FULL>
+template <int NPL, bool FULL, bool PLAIN>
 __device__ __forceinline__ void route_token(const RouteGroupedArgs& a, int t, char* sm) {
   const int lane = threadIdx.x & 31;
   const float* row = a.logits + (size_t)t * a.E;
   int my_e = 0;
   float w = 0.0f, M = 0.0f, sum = 0.0f;
-  if (route_fast<NPL, FULL>(a, row, sm, my_e, M, sum)) {
+  if (route_fast<NPL, FULL, PLAIN>(a, row, sm, my_e, M, sum)) {
     if (lane < a.k) {
       const float l = row[my_e];
       w = a.sigmoid ? __fdiv_rn(1.0f, 1.0f + expf(-l)) : exp2_of(fmaf(l, kLog2e, -M));
@@ -548,13 +557,13 @@ __device__ __forceinline__ void route_token(const RouteGroupedArgs& a, int t, ch
   }
 }
 
-template <int NPL, bool FULL>
-__global__ void __launch_bounds__(256) route_grouped_kernel(const __grid_constant__ RouteGroupedArgs a) {
+template <int NPL, bool FULL, bool PLAIN>
+__global__ void __launch_bounds__(256, PLAIN && NPL <= 16 ? 5 : 1) route_grouped_kernel(const __grid_constant__ RouteGroupedArgs a) {
   extern __shared__ __align__(16) char route_smem[];
   const int warp = threadIdx.x >> 5, t = blockIdx.x * (blockDim.x >> 5) + warp;
   pdl_wait();
   pdl_launch_dependents();
-  if (t < a.T) route_token<NPL, FULL>(a, t, route_smem + warp * warp_bytes(a.E));
+  if (t < a.T) route_token<NPL, FULL, PLAIN>(a, t, route_smem + warp * warp_bytes(a.E));
 }
 
 // One decode token: its routing by warp 0, then the sort and the slot lookup
@@ -565,17 +574,22 @@ __global__ void __launch_bounds__(256)
   extern __shared__ __align__(16) char route_smem[];
   pdl_wait();
   pdl_launch_dependents();
-  if (threadIdx.x < 32) route_token<NPL, FULL>(a, 0, route_smem);
+  if (threadIdx.x < 32) route_token<NPL, FULL, false>(a, 0, route_smem);
   sort_lookup_token(a.ids, a.k + a.ns, a.E + a.ns, o);
+}
+
+template <int NPL, bool FULL>
+const void* route_kernel_of(const RouteGroupedArgs& a, bool sort) {
+  if (sort) return reinterpret_cast<const void*>(route_grouped_sort_lookup_kernel<NPL, FULL>);
+  if (!a.bias && !(a.L > 0.0f) && a.top == a.G)
+    return reinterpret_cast<const void*>(route_grouped_kernel<NPL, FULL, true>);
+  return reinterpret_cast<const void*>(route_grouped_kernel<NPL, FULL, false>);
 }
 
 template <int NPL>
 const void* route_kernel_of(const RouteGroupedArgs& a, bool sort) {
-  if (a.E == 32 * NPL && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0)
-    return sort ? reinterpret_cast<const void*>(route_grouped_sort_lookup_kernel<NPL, true>)
-                : reinterpret_cast<const void*>(route_grouped_kernel<NPL, true>);
-  return sort ? reinterpret_cast<const void*>(route_grouped_sort_lookup_kernel<NPL, false>)
-              : reinterpret_cast<const void*>(route_grouped_kernel<NPL, false>);
+  return a.E == 32 * NPL && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 ? route_kernel_of<NPL, true>(a, sort)
+                                                                            : route_kernel_of<NPL, false>(a, sort);
 }
 
 const void* route_kernel_of(const RouteGroupedArgs& a, bool sort) {

@@ -320,34 +320,34 @@ def route_config(score="softmax", n_groups=1, top_groups=1, group_top=1, renorma
 def moe_route_grouped(logits, T, d, config: RouteConfig, bias, L, slot_table, n_shared, shared_w, ids, w,
                       stream=None) -> None:
     """Top-k by softmax or sigmoid scores with a bias and groups; outputs as moe_route_shared."""
-    _ck(lib().moe_route_grouped(_ptr(logits), int(T), C.byref(d), None if config is None else C.byref(config),
-                                _ptr(bias), float(L), _ptr(slot_table), int(n_shared), _ptr(shared_w), _ptr(ids),
+    _ck(lib().moe_route_grouped(_ptr(logits), T, C.byref(d), None if config is None else C.byref(config),
+                                _ptr(bias), L, _ptr(slot_table), n_shared, _ptr(shared_w), _ptr(ids),
                                 _ptr(w), _stream(stream)), "moe_route_grouped")
 
 
 def moe_add_norm_quant(h, h_type, delta, delta_type, gamma, eps, T, H, h_out, x, q, q_scale, stream=None) -> None:
     """Residual sum, RMS norm (bf16 x) and the norm's 8-bit codes with a scale per row."""
-    _ck(lib().moe_add_norm_quant(_ptr(h), int(h_type), _ptr(delta), int(delta_type), _ptr(gamma), float(eps), int(T),
-                                 int(H), _ptr(h_out), _ptr(x), _ptr(q), _ptr(q_scale), _stream(stream)),
+    _ck(lib().moe_add_norm_quant(_ptr(h), h_type, _ptr(delta), delta_type, _ptr(gamma), eps, T,
+                                 H, _ptr(h_out), _ptr(x), _ptr(q), _ptr(q_scale), _stream(stream)),
         "moe_add_norm_quant")
 
 
 def moe_quantize_channels(w, w_type, rows, K, q, scale, stream=None) -> None:
     """8-bit codes of plain rows, one scale per row."""
-    _ck(lib().moe_quantize_channels(_ptr(w), int(w_type), int(rows), int(K), _ptr(q), _ptr(scale), _stream(stream)),
+    _ck(lib().moe_quantize_channels(_ptr(w), w_type, rows, K, _ptr(q), _ptr(scale), _stream(stream)),
         "moe_quantize_channels")
 
 
 def moe_swiglu_quant(gu, gu_type, T, I, q, q_scale, stream=None) -> None:
     """silu(gate) * up of rows [gate | up], as 8-bit codes with a scale per row."""
-    _ck(lib().moe_swiglu_quant(_ptr(gu), int(gu_type), int(T), int(I), _ptr(q), _ptr(q_scale), _stream(stream)),
+    _ck(lib().moe_swiglu_quant(_ptr(gu), gu_type, T, I, _ptr(q), _ptr(q_scale), _stream(stream)),
         "moe_swiglu_quant")
 
 
 def moe_int_matmul(xq, x_scale, T, wq, w_scale, N, K, add, row_w, y, y_type, dev_err, stream=None) -> None:
     """y = add + row_w x_scale w_scale (xq . wq^T), int32 accumulation."""
-    _ck(lib().moe_int_matmul(_ptr(xq), _ptr(x_scale), int(T), _ptr(wq), _ptr(w_scale), int(N), int(K), _ptr(add),
-                             _ptr(row_w), _ptr(y), int(y_type), _ptr(dev_err), _stream(stream)), "moe_int_matmul")
+    _ck(lib().moe_int_matmul(_ptr(xq), _ptr(x_scale), T, _ptr(wq), _ptr(w_scale), N, K, _ptr(add),
+                             _ptr(row_w), _ptr(y), y_type, _ptr(dev_err), _stream(stream)), "moe_int_matmul")
 
 
 # ---------------------------------------------------------------------------
