@@ -366,7 +366,8 @@ moe_status moe_router_logits(const uint16_t* x, int32_t T, const uint16_t* W, co
  * resident: BigMoeOnEdge docs/limitations.md, "Limitations").  They keep no
  * state and take no workspace: any number of calls may run at once, on any
  * streams and in any captured graphs, as long as their buffers are their own.
- * Outputs may not overlap inputs except where a call says so.
+ * Outputs may not overlap inputs except where a call says so.  What a call
+ * gives for a row does not depend on the other rows, nor on how many there are.
  * ---------------------------------------------------------------------- */
 
 /* Element types of the calls below. */
@@ -442,7 +443,8 @@ moe_status moe_quantize_channels(const void* w, int32_t w_type, int32_t rows, in
                                  cudaStream_t stream);
 
 /* SwiGLU with 8-bit codes: v = silu(gate) up in fp32, a = max |v| of the row,
- * q = rint(127 v / a), q_scale = a / 127.
+ * q = rint(127 v / a), q_scale = a / 127.  (exp(-|gate|) below 2^-126 counts
+ * as 0.)
  *   gu     device [T, 2I] of gu_type: a row's I gate values, then its I up
  *          values; 16-byte aligned; I a multiple of 8, at most 65536
  *   q      device int8 [T, I], 8-byte aligned;  q_scale  device fp32 [T]

@@ -27,10 +27,14 @@
 namespace moe {
 namespace {
 
-__device__ __forceinline__ float im_scaled(int acc, float xs, float ws) { return (float)acc * (xs * ws); }
+// Products rounded one by one (never joined with the sum that follows): every
+// kernel gives an output the same bits.
+__device__ __forceinline__ float im_scaled(int acc, float xs, float ws) {
+  return __fmul_rn((float)acc, __fmul_rn(xs, ws));
+}
 
 __device__ __forceinline__ float im_token_scale(const IntMatmulArgs& a, int t) {
-  return a.row_w ? a.xs[t] * a.row_w[t] : a.xs[t];
+  return a.row_w ? __fmul_rn(a.xs[t], a.row_w[t]) : a.xs[t];
 }
 
 __device__ __forceinline__ void im_store(const IntMatmulArgs& a, int t, int n, float v) {
@@ -50,7 +54,7 @@ __device__ __forceinline__ void im_store(const IntMatmulArgs& a, int t, int n, f
 // 4096 x 2048 in 5.3 and 5.9, x 4096 x 8192 in 10.8 and 10.3.
 constexpr int kRowsTokens = 16, kRowsMaxTokens = 32;
 constexpr int64_t kRowsMaxWeights = 1 << 23;
-// 128-input units a warp keeps in flight; the registers hold fewer next to two token tiles
+// 128-input units a warp keeps in flight; the registers hold fewer next to more token tiles
 __host__ __device__ constexpr int rows_depth(int nt) { return nt == 1 ? 4 : nt == 2 ? 2 : 1; }
 
 // D (16 x 8, s32) += A (16 x 32, s8, row) . B (32 x 8, s8, column).
