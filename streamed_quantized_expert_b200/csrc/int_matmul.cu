@@ -554,6 +554,11 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
       "h"((uint16_t)3)
       : "memory");
 }
+// The same for this CTA's barrier alone.
+__device__ __forceinline__ void umma_commit_pair_local(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -673,7 +678,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
       }
       if (issued_any) {  // every MMA issued completes before TMEM is freed
-        umma_commit_pair(drain);
+        // its arrival is waited for here only, so it must not reach the other CTA, which may have gone
+        umma_commit_pair_local(drain);
         mbar_wait_bounded(drain, 0, exit_limit(a));
       }
     }

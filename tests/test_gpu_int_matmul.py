@@ -176,3 +176,22 @@ def test_two_calls_at_once(T, N, K):
     for a, b in zip(sets, bufs):
         check(b[4].cpu().numpy(), *a, True)
         assert int(b[5].item()) == 0
+
+
+@pytest.mark.parametrize("T,N,K", [(40, 300, 2064), (100, 9602, 1040), (513, 4099, 1040), (700, 7001, 4112)])
+def test_waits_that_may_run_out(T, N, K):
+    """With the shortest limit a wait runs out or does not, as the copies
+    land: the call returns, reports no error but MOE_DEV_ERR_TIMEOUT, and the
+    next call with the default limit is right."""
+    a = inputs(4, T, N, K, False, False)
+    b = [dev(x) for x in a[:4]]
+    y, err = torch.empty((T, N), device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    try:
+        ops.moe_set_wait_limit_cycles(1)
+        for _ in range(3):
+            ops.moe_int_matmul(b[0], b[1], T, b[2], b[3], N, K, None, None, y, ops.MOE_F32, err)
+        torch.cuda.synchronize()
+    finally:
+        ops.moe_set_wait_limit_cycles(0)
+    assert int(err.item()) in (0, ops.DEV_ERR_TIMEOUT)
+    check(run(*a, True), *a, True)
