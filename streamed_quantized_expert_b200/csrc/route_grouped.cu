@@ -229,12 +229,12 @@ __device__ __forceinline__ float max_abs3(float m, float a, float b) {  // NaN i
 
 // The token's choice in fp32, or of the candidates that fp32 leaves in 64
 // bits; false where that does not settle it.  my_e: lane j's expert (rank j);
-// M, sum: the softmax's exponent offset and denominator.  FULL: E = 32 NPL,
+// lmax, sum: the largest logit and the softmax's denominator.  FULL: E = 32 NPL,
 // and the lanes hold four experts side by side.  PLAIN: no bias, substitution
-// or groups (code and registers of their own: 16384 x 512 takes 13.0 us, 16.1
+// or groups (code and registers of their own: 16384 x 512 takes 13.4 us, 16.1
 // with all of it in one kernel).
 template <int NPL, bool FULL, bool PLAIN>
-__device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const float* row, char* sm, int& my_e, float& M,
+__device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const float* row, char* sm, int& my_e, float& lmax,
                                            float& sum) {
   const int lane = threadIdx.x & 31, E = a.E, k = a.k;
   const bool lifted = !PLAIN && a.L > 0.0f && a.table, by_l = PLAIN || (!a.bias && !lifted);
@@ -266,37 +266,36 @@ __device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const floa
 #pragma unroll
     for (int i = 0; i < NPL; ++i) resident |= (have(i) && a.table[expert(i)] >= 0 ? 1u : 0u) << i;
   }
-  float big = 0.0f, lmax = -INFINITY;
+  float big = 0.0f;
+  lmax = -INFINITY;
 #pragma unroll
   for (int i = 0; i < NPL; i += 2) {
     big = max_abs3(big, have(i) ? key[i] : 0.0f, have(i + 1) ? key[i + 1] : 0.0f);
     lmax = max3(lmax, key[i], key[i + 1]);
   }
   if (__any_sync(kAll, !(big < INFINITY))) return false;  // an expert that is off, or a logit without order
-  M = sum = 0.0f;
+  sum = 0.0f;
   float D = 0.0f, inv = 1.0f, lift = 0.0f, most = 0.0f, hi = -INFINITY, lo = -INFINITY;  // lo: of -c at first
-  if (!a.sigmoid) {
-    M = warp_max(lmax) * kLog2e;
-    if (!(fabsf(M) < 65536.0f)) return false;  // its rounding, which all terms share, would leave 2^x's range
-  }
+  if (!a.sigmoid) lmax = warp_max(lmax);
   // a score before the softmax's quotient; every rounding is spelled out, so
   // that the candidates' c are the same numbers when they are computed again
   auto term = [&](float l) {
-    return a.sigmoid ? rcp(__fadd_rn(1.0f, exp2_of(__fmul_rn(l, -kLog2e)))) : exp2_of(__fmaf_rn(l, kLog2e, -M));
+    return a.sigmoid ? rcp(__fadd_rn(1.0f, exp2_of(__fmul_rn(l, -kLog2e))))
+                     : exp2_of(__fmul_rn(__fsub_rn(l, lmax), kLog2e));
   };
   if (by_l && !groups) {
     if (!a.sigmoid && !a.renorm) {
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) sum += exp2_of(fmaf(key[i], kLog2e, -M));  // 0 past E
+      for (int i = 0; i < NPL; ++i) sum += term(key[i]);  // 0 past E
       sum = warp_sum(sum);
     }
   } else {
     // How far a score may be off, in 2^-24: 1 / (1 + 2^x) with x rounded once
     // and 2^x off by 2^-22: 1 (of 2^x, halved twice) + 1/4 (of x) + 1 + 2 (the
-    // sum, the reciprocal).  A softmax's terms are off by 4 + |x| (|x| 2^x stays
-    // below 1), its sum by as much, |x| below log2 E on the average, and by a
-    // tree of additions, its quotient by 3: 36 of the largest.  The sum's error
-    // is every score's and does not count where no bias is added: 8.
+    // sum, the reciprocal).  A softmax's terms are off by 4 + 1.4 |x| (|x| 2^x
+    // stays below 1), its sum by as much, |x| below log2 E on the average, and
+    // by a tree of additions, its quotient by 3: 40 of the largest.  The sum's
+    // error is every score's and does not count where no bias is added: 8.
     float s[NPL], unit = 5.0f * 0x1p-24f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) s[i] = term(key[i]);
@@ -312,7 +311,7 @@ __device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const floa
       inv = rcp(sum);
 #pragma unroll
       for (int i = 0; i < NPL; ++i) s[i] = __fmul_rn(s[i], inv);
-      unit = (a.bias ? 36.0f : 8.0f) * 0x1p-24f * inv;
+      unit = (a.bias ? 40.0f : 8.0f) * 0x1p-24f * inv;
     }
     if (a.bias) {  // c, before the lift
 #pragma unroll
@@ -481,7 +480,7 @@ __device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const floa
   // the candidates in 64 bits, if none that is not among them can be better than the k-th
   if (!(tau == -FLT_MAX || skey[k - 1] - tau > 2.0f * D)) return false;
   double total = 1.0;
-  const double lm = (double)warp_max(lmax);
+  const double lm = (double)lmax;
   if (!a.sigmoid) {
     total = 0.0;
 #pragma unroll 4
@@ -531,14 +530,26 @@ __device__ __forceinline__ void route_token(const RouteGroupedArgs& a, int t, ch
   const int lane = threadIdx.x & 31;
   const float* row = a.logits + (size_t)t * a.E;
   int my_e = 0;
-  float w = 0.0f, M = 0.0f, sum = 0.0f;
-  if (route_fast<NPL, FULL, PLAIN>(a, row, sm, my_e, M, sum)) {
+  float w = 0.0f, lmax = 0.0f, sum = 0.0f;
+  if (route_fast<NPL, FULL, PLAIN>(a, row, sm, my_e, lmax, sum)) {
+    const float l = lane < a.k ? row[my_e] : 0.0f;
     if (lane < a.k) {
-      const float l = row[my_e];
-      w = a.sigmoid ? __fdiv_rn(1.0f, 1.0f + expf(-l)) : exp2_of(fmaf(l, kLog2e, -M));
+      if (a.sigmoid) {
+        w = __fdiv_rn(1.0f, 1.0f + expf(-l));
+      } else {  // exp(l - lmax) with what the difference's rounding leaves out
+        const float d = __fsub_rn(l, lmax), b = __fsub_rn(d, l);
+        const float rest = __fsub_rn(__fsub_rn(l, __fsub_rn(d, b)), __fadd_rn(lmax, b)), p = expf(d);
+        w = fmaf(p, rest, p);
+      }
     }
-    const float den = a.renorm ? warp_sum(w) : a.sigmoid ? 1.0f : sum;
-    w = den > 0.0f ? a.scale * __fdiv_rn(w, den) : 0.0f;
+    if (__any_sync(kAll, lane < a.k && !(w > 0x1p-100f))) {  // scores that fp32 hardly holds, or not
+      const double s = lane >= a.k ? 0.0 : a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)lmax);
+      const double den = a.renorm ? warp_sum(s) : a.sigmoid ? 1.0 : (double)sum;
+      w = den > 0.0 ? (float)((double)a.scale * (s / den)) : 0.0f;
+    } else {
+      const float den = a.renorm ? warp_sum(w) : a.sigmoid ? 1.0f : sum;
+      w = a.scale * __fdiv_rn(w, den);
+    }
   } else {
     double s = 0.0;
     __syncwarp();

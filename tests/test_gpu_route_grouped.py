@@ -234,3 +234,28 @@ def test_logits_at_an_odd_address():
     ops.moe_route_grouped(buf[3:], T, d, ops.route_config("sigmoid", 8, 4, 2), None, 0.0, None, 0, None, ids, w)
     torch.cuda.synchronize()
     assert np.array_equal(ids.cpu().numpy(), ref.route(logits, k, True, None, 8, 4, 2)[0])
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,E,k,G,top,gtop", [(40, 64, 24, 1, 1, 1), (17, 512, 32, 1, 1, 1), (33, 128, 30, 8, 4, 2)])
+def test_weights_far_below_the_largest(score, renorm, T, E, k, G, top, gtop):
+    """A weight keeps its own relative precision: exp(l - max) of a difference
+    of a hundred, where an exponent rounded once is off by |x| half steps."""
+    logits = 30.0 * synth.router_logits(5, 0, T, E)
+    check(logits, k, score, None, G, top, gtop, renorm)
+    check(logits - 80.0, k, score, None, G, top, gtop, renorm)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_renormalised_scores_below_fp32(score):
+    """A bias that chooses experts whose scores are far below fp32's range:
+    they are still renormalised to their sum."""
+    E, k = 64, 4
+    r = np.random.default_rng(4)
+    logits = (synth.router_logits(6, 0, 9, E) - 120.0).astype(np.float32)
+    logits[:, :8] = r.uniform(20, 30, (9, 8))
+    b = np.where(np.arange(E) < 8, -10.0, 0.0).astype(np.float32)
+    b[20:24] = 10.0
+    ids, w = check(logits, k, score, b)
+    assert (np.sort(ids, axis=1) == np.arange(20, 24)).all() and np.abs(w.sum(axis=1) - 1).max() <= 8 * ref.U32
