@@ -389,7 +389,8 @@ typedef struct {
  * For each token, over reals (equal values go to the lower id or group):
  *   s_e = softmax(l)_e or sigmoid(l_e);  c_e = s_e + bias_e
  *   L > 0: c_e += L (max c - min c) for resident e (the cache-aware
- *     substitution of moe_route, in the score that chooses)
+ *     substitution of moe_route, in the score that chooses), summed as
+ *     max c + ((c_e - min c) + (L - 1) (max c - min c)): exact ties at L = 1
  *   the top_groups groups by the sum of their group_top best c are kept
  *   ids: the k best of the kept groups by (c desc, l desc, e asc)
  *   w_j = scale s_e, or scale s_e / sum of the chosen s (renormalise; 0 where

@@ -20,7 +20,7 @@
 //
 // What bounds it: instructions, 545 a token of 512 experts (its 2 KB would take
 // 0.3 ns at 6.6 TB/s), and for a few thousand tokens their latency.  16384
-// tokens x 512 experts, softmax, k 10: 13.0 us; 4096 x 256, sigmoid with bias
+// tokens x 512 experts, softmax, k 10: 13.4 us; 4096 x 256, sigmoid with bias
 // and 4 of 8 groups, k 8: 8.2-8.9 us; one token of 512 with all of it: 4.3 us
 // (243, 53 and 41 us where every score and choice is made in 64 bits with a
 // search of all experts per rank).
@@ -86,6 +86,13 @@ __device__ __forceinline__ float logit(const float* row, int e) {
   return l == l ? l : -INFINITY;
 }
 
+// c + L (hi - lo) of a resident expert.  At L = 1 the lowest of them meets the
+// highest score over the reals; summed from hi downwards that tie is exact in
+// 64 bits too and goes to the larger logit, not to the way the sum rounds.
+__device__ __forceinline__ double lift_of(double c, float L, double hi, double lo) {
+  return hi > lo ? __dadd_rn(hi, __dadd_rn(__dsub_rn(c, lo), __dmul_rn((double)L - 1.0, __dsub_rn(hi, lo)))) : c;
+}
+
 // The token's choice in 64 bits: lane j (< k) gets rank j's expert and score.
 // c: E doubles of shared memory of this warp.
 __device__ __noinline__ void route_exact(const RouteGroupedArgs& a, const float* row, double* c, int& my_e,
@@ -122,9 +129,8 @@ __device__ __noinline__ void route_exact(const RouteGroupedArgs& a, const float*
   if (a.L > 0.0f && a.table) {
     hi = warp_max(hi);
     lo = -warp_max(lo);
-    const double lift = hi > lo ? __dmul_rn((double)a.L, hi - lo) : 0.0;
     for (int e = lane; e < E; e += 32)
-      if (c[e] != -INFINITY && a.table[e] >= 0) c[e] = __dadd_rn(c[e], lift);
+      if (c[e] != -INFINITY && a.table[e] >= 0) c[e] = lift_of(c[e], a.L, hi, lo);
   }
   __syncwarp();
   if (a.top < a.G) {
@@ -492,9 +498,8 @@ __device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const floa
     const double l = (double)row[e], v = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - lm) * quotient;
     return a.bias ? v + (double)a.bias[e] : v;
   };
-  double lift64 = 0.0;
+  double top64 = -INFINITY, low64 = -INFINITY;  // low64: of -c at first
   if (lifted) {
-    double top64 = -INFINITY, low64 = -INFINITY;  // low64: of -c
     for (int e = lane; e < E; e += 32) {
       float c = term(row[e]);
       if (!a.sigmoid) c = __fmul_rn(c, inv);
@@ -504,13 +509,12 @@ __device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const floa
     }
     top64 = warp_max(top64);
     low64 = -warp_max(low64);
-    lift64 = top64 > low64 ? __dmul_rn((double)a.L, top64 - low64) : 0.0;
   }
   __syncwarp();
   for (int j = lane; j < cnt; j += 32) {
     const int e = cand[j];
     const double c = exact(e);
-    wide[j] = Cand{lifted && a.table[e] >= 0 ? __dadd_rn(c, lift64) : c, row[e], e};
+    wide[j] = Cand{lifted && a.table[e] >= 0 ? lift_of(c, a.L, top64, low64) : c, row[e], e};
   }
   __syncwarp();
   for (int j = lane; j < cnt; j += 32) {

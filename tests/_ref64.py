@@ -35,9 +35,10 @@ def route(logits, k, sigmoid, bias=None, G=1, top=1, gtop=1, renorm=True, scale=
     if L > 0:
         hi = np.where(off, -np.inf, c).max(axis=1)
         lo = np.where(off, np.inf, c).min(axis=1)
+        # c + L (hi - lo), from hi downwards: at L = 1 the lowest meets hi exactly
         with np.errstate(invalid="ignore"):
-            lift = np.where(hi > lo, np.float64(np.float32(L)) * (hi - lo), 0.0)
-        c = np.where((np.asarray(table)[:E] >= 0)[None, :] & ~off, c + lift[:, None], c)
+            up = hi[:, None] + ((c - lo[:, None]) + (np.float64(np.float32(L)) - 1.0) * (hi - lo)[:, None])
+        c = np.where((np.asarray(table)[:E] >= 0)[None, :] & ~off & (hi > lo)[:, None], up, c)
     m = E // G
     ids, w = np.zeros((T, k), np.int32), np.zeros((T, k))
     for t in range(T):

@@ -259,3 +259,16 @@ def test_renormalised_scores_below_fp32(score):
     b[20:24] = 10.0
     ids, w = check(logits, k, score, b)
     assert (np.sort(ids, axis=1) == np.arange(20, 24)).all() and np.abs(w.sum(axis=1) - 1).max() <= 8 * ref.U32
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("T,E,k,G,top,gtop", [(200, 4, 1, 4, 1, 1), (200, 8, 6, 1, 1, 1), (60, 64, 24, 8, 4, 2),
+                                              (60, 256, 32, 1, 1, 1), (40, 48, 32, 1, 1, 1)])
+def test_full_substitution_ties_the_lowest_with_the_highest(score, bias, T, E, k, G, top, gtop):
+    """L = 1 lifts the lowest score to the highest exactly: the larger logit goes first."""
+    r = np.random.default_rng(E)
+    b = (0.1 * r.standard_normal(E)).astype(np.float32) if bias else None
+    for step, logits in enumerate([synth.router_logits(8, 0, T, E), np.round(synth.router_logits(8, 1, T, E) * 4) / 4]):
+        table = np.where(r.random(E) < 0.5, r.integers(0, 50, E), -1).astype(np.int32)
+        check(logits.astype(np.float32), k, score, b, G, top, gtop, True, 1.0, 1.0, table)
