@@ -474,12 +474,19 @@ __device__ __forceinline__ bool route_fast(const RouteGroupedArgs& a, const floa
   my_e = lane < k ? sid[lane] : 0;
   bool ok = true;
   if (!by_l && lane < k && lane + 1 < cnt) {
-    const float gap = skey[lane] - skey[lane + 1];
-    ok = gap > 2.0f * D;
-    if (gap == 0.0f) {  // two experts alike in all that counts: the lower one first, as they are
-      const int e = my_e, f = sid[lane + 1];
-      ok = row[e] == row[f] && (!a.bias || a.bias[e] == a.bias[f]) &&
-           (!lifted || (a.table[e] >= 0) == (a.table[f] >= 0));
+    // alike in all that counts: the lower one first, as they are
+    auto alike = [&](int f) {
+      return row[my_e] == row[f] && (!a.bias || a.bias[my_e] == a.bias[f]) &&
+             (!lifted || (a.table[my_e] >= 0) == (a.table[f] >= 0));
+    };
+    ok = skey[lane] - skey[lane + 1] > 2.0f * D;
+    if (skey[lane] == skey[lane + 1]) {
+      ok = alike(sid[lane + 1]);
+      if (ok && lane == k - 1) {  // those behind the last place that are alike, then the first that is not
+        int j = k + 1;
+        while (j < cnt && skey[j] == skey[lane] && alike(sid[j])) ++j;
+        ok = j < cnt ? skey[lane] - skey[j] > 2.0f * D : tau == -FLT_MAX || skey[lane] - tau > 2.0f * D;
+      }
     }
   }
   if (__all_sync(kAll, ok)) return true;

@@ -272,3 +272,42 @@ def test_full_substitution_ties_the_lowest_with_the_highest(score, bias, T, E, k
     for step, logits in enumerate([synth.router_logits(8, 0, T, E), np.round(synth.router_logits(8, 1, T, E) * 4) / 4]):
         table = np.where(r.random(E) < 0.5, r.integers(0, 50, E), -1).astype(np.int32)
         check(logits.astype(np.float32), k, score, b, G, top, gtop, True, 1.0, 1.0, table)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,twins", [(31, 5, 2), (64, 9, 2), (256, 8, 4), (512, 20, 3)])
+def test_a_third_expert_behind_twins_at_the_last_place(score, E, k, twins):
+    """The last place falls between experts alike in logit and bias, and one that
+    differs in both comes within a few steps of fp32 of them: it is compared too."""
+    r = np.random.default_rng(E + k)
+    T, sig = 96, score == "sigmoid"
+    logits = r.uniform(-4, -2, (T, E)).astype(np.float32)
+    b = np.zeros(E, np.float32)
+    logits[:, :k - 1] = r.uniform(3, 4, (T, k - 1))
+    b[:k - 1] = 1.0
+    pair, third = np.arange(k - 1, k - 1 + twins), E - 1
+    logits[:, pair] = r.uniform(-1, 1, (T, 1))
+    b[pair], b[third] = 0.5, 0.5 - 2.0**-9
+    for _ in range(30):  # the logit that makes the third's score theirs, then some steps off it
+        s = ref.route(logits, k, sig, None)[2]
+        want = s[:, pair[0]] + np.float64(b[pair[0]]) - np.float64(b[third])
+        if sig:
+            logits[:, third] = np.log(want / (1 - want))
+        else:
+            rest = np.delete(np.exp(logits.astype(np.float64)), third, axis=1).sum(axis=1)
+            logits[:, third] = np.log(want * rest / (1 - want))
+    steps = np.arange(T) % 9 - 4
+    l3 = logits[:, third]
+    logits[:, third] = l3 + steps * np.spacing(np.abs(l3)) * np.sign(np.abs(l3))
+    assert np.isfinite(logits).all()
+    ids, _ = check(logits, k, score, b)
+    assert 0 < (ids == third).any(axis=1).sum() < T  # both sides are met
+
+
+@pytest.mark.parametrize("E,k", [(31, 10), (40, 12), (64, 20)])
+def test_full_substitution_with_equal_lowest_scores(E, k):
+    r = np.random.default_rng(k)
+    for step in range(4):
+        logits = (np.round(synth.router_logits(9, step, 340, E) * 4) / 4).astype(np.float32)
+        check(logits, k, "softmax", None, 1, 1, 1, False, 2.5, 1.0,
+              np.where(r.random(E) < k / E, r.integers(0, 50, E), -1).astype(np.int32))
