@@ -124,6 +124,9 @@ class Streamer:
         self.k = layers[0].desc.k
         self.H = layers[0].desc.H
         assert all(l.desc.E == self.E and l.desc.H == self.H for l in layers)
+        assert all(l.route_bias is None or (l.route is not None and l.route_bias.dtype == torch.float32
+                                            and l.route_bias.is_contiguous() and l.route_bias.numel() == self.E)
+                   for l in layers)
         self.ns = n_shared
         assert n_shared == 0 or all(l.shared is not None and l.shared.shape[0] == n_shared for l in layers)
         self.Ew, self.kw = self.E + n_shared, self.k + n_shared  # the widened layer
@@ -429,6 +432,23 @@ class Streamer:
             self.ffn(layer, x, T, p, PASS_EXPERTS, y)
         return y
 
+    def _block_fits(self, spec, h, delta, T: int, row_w, y) -> bool:
+        """Whether block can read and write all that it is given."""
+        bits = (torch.bfloat16, torch.int16, torch.uint16)
+
+        def holds(t, n, *types):
+            return t.is_cuda and t.is_contiguous() and t.numel() >= n and t.dtype in types
+
+        n, gamma, router = T * self.H, spec.norm, spec.router
+        return (gamma is not None and router is not None
+                and gamma.numel() == self.H and holds(gamma, self.H, *bits)
+                and tuple(router.shape) == (self.E, self.H) and holds(router, 0, *bits)
+                and holds(h, n, torch.float32, *bits)
+                and (delta is None or holds(delta, n, torch.float32, *bits))
+                and (row_w is None or holds(row_w, T, torch.float32))
+                and (y is None or holds(y, n, torch.float32))
+                and (spec.always is None or spec.always.H == self.H))
+
     def block(self, layer: int, h: torch.Tensor, delta, T: int, L: float = 0.0, eps: float = 1e-6, prefill=None,
               row_w=None, y=None):
         """One layer around its experts, on self.stream: h [T, H] (bf16 or fp32,
@@ -437,11 +457,15 @@ class Streamer:
         scores the result; the routed experts run (prefill_layer, by default
         above 64 tokens, else decode_layer) and the always-on expert, if the
         layer has one, adds its output (times row_w [T] fp32).  Returns y fp32
-        [T, H], the next block's delta."""
-        spec, s = self.layers[layer], self.stream
-        if T < 1 or T > self.max_tokens:
+        [T, H], the next block's delta.  L counts in decode_layer alone.  What
+        is refused leaves h as it was; where the slot cache turns out too small
+        for the chosen experts, h has taken delta."""
+        spec, s, always = self.layers[layer], self.stream, self.layers[layer].always
+        if prefill is None:
+            prefill = T > 64
+        if T < 1 or T > self.max_tokens or (always is not None and T > always.max_tokens):
             raise ops.MoeError(ops.MOE_ERR_CAPACITY, "Streamer.block")
-        if spec.norm is None or spec.router is None or any(t is not None and t.numel() < T * self.H for t in (h, delta)):
+        if (T > 64 and not prefill) or not self._block_fits(spec, h, delta, T, row_w, y):
             raise ops.MoeError(ops.MOE_ERR_INVALID, "Streamer.block")
         if self.x is None:
             new = lambda *shape, dt: torch.empty(shape, dtype=dt, device=self.device)  # noqa: E731
@@ -450,19 +474,19 @@ class Streamer:
             self.x_scale = new(self.max_tokens, dt=torch.float32)
             self.logits = new(self.max_tokens, self.E, dt=torch.float32)
             s.wait_stream(torch.cuda.current_stream(self.device))  # the buffers' memory comes from there
-        codes = spec.always is not None
+        codes = always is not None
         ops.moe_add_norm_quant(h, _kind(h), delta, ops.MOE_BF16 if delta is None else _kind(delta), spec.norm, eps, T,
                                self.H, h if delta is not None else None, self.x, self.xq if codes else None,
                                self.x_scale if codes else None, s)
         ops.moe_router_logits(self.x, T, spec.router, None, 1.0, self.E, self.H, self.logits, s)
         self.launches += 2
-        if (T > 64) if prefill is None else prefill:
+        if prefill:
             y = self.prefill_layer(layer, self.x, self.logits, T, y)
         else:
             y = self.decode_layer(layer, self.x, self.logits, T, L, y)
         if codes:
-            spec.always.add(self.xq, self.x_scale, T, y, self.dev_err, row_w, s)
-            self.launches += spec.always.LAUNCHES
+            always.add(self.xq, self.x_scale, T, y, self.dev_err, row_w, s)
+            self.launches += always.LAUNCHES
         return y
 
     def check_dev_err(self) -> int:

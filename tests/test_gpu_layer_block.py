@@ -208,3 +208,46 @@ def test_block_refuses_too_many_tokens(orc):
     with pytest.raises(ops.MoeError) as ei:
         st.layers[0].always.add(h, h, 257, h, None)
     assert ei.value.status == ops.MOE_ERR_CAPACITY
+
+
+def test_a_refused_block_leaves_h_as_it_was(orc):
+    """What a block could not run, or would read past, is refused before h takes delta."""
+    st, _, _ = layers(orc, 1, 24)
+    spec = st.layers[0]
+    h = torch.ones((256, H), dtype=torch.bfloat16, device="cuda")
+    delta = torch.ones((256, H), device="cuda")
+    good = spec.always, spec.norm, spec.router
+    small = IntExpert(torch.ones((64, H), device="cuda"), torch.ones((H, 32), device="cuda"), 2)
+    narrow = IntExpert(torch.ones((64, H // 2), device="cuda"), torch.ones((H // 2, 32), device="cuda"), 256)
+
+    def refused(status, T=3, spec_values=good, **kw):
+        spec.always, spec.norm, spec.router = spec_values
+        try:
+            with pytest.raises(ops.MoeError) as ei:
+                st.block(0, h, delta, T, **kw)
+        finally:
+            spec.always, spec.norm, spec.router = good
+        assert ei.value.status == status
+        torch.cuda.synchronize()
+        assert (h == 1).all()
+
+    refused(ops.MOE_ERR_CAPACITY, spec_values=(small, *good[1:]))
+    refused(ops.MOE_ERR_INVALID, spec_values=(narrow, *good[1:]))
+    refused(ops.MOE_ERR_INVALID, T=65, prefill=False)
+    for norm in (None, good[1][:8], good[1].float(), good[1].cpu()):
+        refused(ops.MOE_ERR_INVALID, spec_values=(good[0], norm, good[2]))
+    for router in (None, good[2][:-1], good[2].t(), good[2].float()):
+        refused(ops.MOE_ERR_INVALID, spec_values=(good[0], good[1], router))
+    w = torch.ones(8, device="cuda")
+    for row_w in (w[:2], w[::2], w.double(), w.cpu()):
+        refused(ops.MOE_ERR_INVALID, row_w=row_w)
+    for y in (torch.empty((2, H), device="cuda"), h[:3], torch.empty((3, H))):
+        refused(ops.MOE_ERR_INVALID, y=y)
+
+
+def test_a_bias_needs_a_routing_that_reads_it(orc):
+    st, _, _ = layers(orc, 1, 24)
+    spec = st.layers[0]
+    for change in (dict(route=None), dict(route_bias=spec.route_bias[:-1]), dict(route_bias=spec.route_bias.double())):
+        with pytest.raises(AssertionError):
+            Streamer([LayerSpec(**{**spec.__dict__, **change})], 24, max_tokens=8)
