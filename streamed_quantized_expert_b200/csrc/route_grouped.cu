@@ -21,7 +21,7 @@
 // What bounds it: instructions, 545 a token of 512 experts (its 2 KB would take
 // 0.3 ns at 6.6 TB/s), and for a few thousand tokens their latency.  16384
 // tokens x 512 experts, softmax, k 10: 13.4 us; 4096 x 256, sigmoid with bias
-// and 4 of 8 groups, k 8: 8.2-8.9 us; one token of 512 with all of it: 4.3 us
+// and 4 of 8 groups, k 8: 7.7 us; one token of 512 with all of it: 4.2 us
 // (243, 53 and 41 us where every score and choice is made in 64 bits with a
 // search of all experts per rank).
 #include <cfloat>
@@ -600,10 +600,12 @@ __global__ void __launch_bounds__(256)
   sort_lookup_token(a.ids, a.k + a.ns, a.E + a.ns, o);
 }
 
+bool is_plain(const RouteGroupedArgs& a) { return !a.bias && !(a.L > 0.0f) && a.top == a.G; }
+
 template <int NPL, bool FULL>
 const void* route_kernel_of(const RouteGroupedArgs& a, bool sort) {
   if (sort) return reinterpret_cast<const void*>(route_grouped_sort_lookup_kernel<NPL, FULL>);
-  if (!a.bias && !(a.L > 0.0f) && a.top == a.G)
+  if (is_plain(a))
     return reinterpret_cast<const void*>(route_grouped_kernel<NPL, FULL, true>);
   return reinterpret_cast<const void*>(route_grouped_kernel<NPL, FULL, false>);
 }
@@ -624,9 +626,14 @@ const void* route_kernel_of(const RouteGroupedArgs& a, bool sort) {
 }  // namespace
 
 cudaError_t launch_route_grouped(const RouteGroupedArgs& a, int num_sms, cudaStream_t st) {
-  // few tokens spread over the SMs; no more than 48 KB of shared memory a block
+  // few tokens spread over the SMs; no more than 48 KB of shared memory a block.
+  // With a bias, groups or substitution a thread takes 68 registers, of which
+  // an SM holds 3 blocks of 8 warps or 7 of 4: 4096 x 256 takes 8.8 / 7.7 us
+  // with blocks of 8 / 4 (one wave), 8192 x 256 13.9 / 12.9, 2048 x 256 6.0 /
+  // 5.6; the plain kernel (48 registers) 13.3 / 14.1 at 16384 x 512.
+  const int most = is_plain(a) ? 8 : 4;
   int warps = a.T / num_sms;
-  warps = warps < 1 ? 1 : warps > 8 ? 8 : warps;
+  warps = warps < 1 ? 1 : warps > most ? most : warps;
   while (warps > 1 && warps * warp_bytes(a.E) > 48 * 1024) --warps;
   return launch_pdl(route_kernel_of(a, false), (a.T + warps - 1) / warps, 32 * warps, warps * warp_bytes(a.E), st, a);
 }

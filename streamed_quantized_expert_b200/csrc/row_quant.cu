@@ -207,9 +207,9 @@ __device__ __forceinline__ float exp2_of(float x) {
 // whose denominator never overflows; the quotient is corrected once, which
 // leaves one rounding.  s = 2^(t + e): t = -|g| log2 e rounded, e what the
 // rounding and the constant's tail leave out, 2^e = 1 + e ln 2 (e < 2^-15).
-// |g| above 128 gives 0 like 128 does.  35 instructions a value with its code
-// bound the call: 4000 x 8200 bf16 takes 48 us, 3.4 TB/s (two lanes to an
-// instruction; 50 us one by one).
+// |g| above 128 gives 0 like 128 does.  24 instructions a value with its code
+// bound the call: 4000 x 8200 bf16 takes 37-41 us, 4.0-4.4 TB/s (two lanes to
+// an instruction).
 __device__ __forceinline__ F2 swiglu_of(F2 g2, F2 u) {
   const float2 g = split2(g2);
   const F2 m = pack2(fminf(fabsf(g.x), 128.0f), fminf(fabsf(g.y), 128.0f)), one = pack2(1.0f, 1.0f);
