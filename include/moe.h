@@ -396,8 +396,8 @@ typedef struct {
  *   w_j = scale s_e, or scale s_e / sum of the chosen s (renormalise; 0 where
  *     that sum is 0)
  * The choice is made in 64-bit arithmetic or proved equal to it.  c, or sums of
- * a group, that are made of different logits or biases and lie within a few
- * steps of 64 bits of one another may go either way.
+ * a group, that lie within a few steps of 64 bits of one another may go either
+ * way, unless their logits, biases and lifts are the same: then they are equal.
  *   logits     device fp32 [T, E].  -inf (or NaN) turns an expert off for the
  *              token: its c is -inf and its s 0, so it is chosen, with weight
  *              0, only when the kept groups have no other expert left

@@ -86,11 +86,14 @@ __device__ __forceinline__ float logit(const float* row, int e) {
   return l == l ? l : -INFINITY;
 }
 
-// c + L (hi - lo) of a resident expert.  At L = 1 the lowest of them meets the
-// highest score over the reals; summed from hi downwards that tie is exact in
-// 64 bits too and goes to the larger logit, not to the way the sum rounds.
-__device__ __forceinline__ double lift_of(double c, float L, double hi, double lo) {
-  return hi > lo ? __dadd_rn(hi, __dadd_rn(__dsub_rn(c, lo), __dmul_rn((double)L - 1.0, __dsub_rn(hi, lo)))) : c;
+// c + L (hi - lo) of a resident expert, or the sum c of n of them.  At L = 1
+// the lowest meets the highest score over the reals; summed from hi downwards
+// that tie is exact in 64 bits too and goes to the larger logit, not to the
+// way the sum rounds.
+__device__ __forceinline__ double lift_of(double c, float L, double hi, double lo, double n = 1.0) {
+  if (!(hi > lo)) return c;
+  const double down = __dmul_rn((double)L - 1.0, __dsub_rn(hi, lo));
+  return __dadd_rn(n * hi, __dadd_rn(__dsub_rn(c, n * lo), n * down));  // n times: exact
 }
 
 // The token's choice in 64 bits: lane j (< k) gets rank j's expert and score.
@@ -126,9 +129,11 @@ __device__ __noinline__ void route_exact(const RouteGroupedArgs& a, const float*
     }
     c[e] = v;
   }
-  if (a.L > 0.0f && a.table) {
+  bool lifted = a.L > 0.0f && a.table;
+  if (lifted) {
     hi = warp_max(hi);
     lo = -warp_max(lo);
+    lifted = hi > lo;
     for (int e = lane; e < E; e += 32)
       if (c[e] != -INFINITY && a.table[e] >= 0) c[e] = lift_of(c[e], a.L, hi, lo);
   }
@@ -150,7 +155,30 @@ __device__ __noinline__ void route_exact(const RouteGroupedArgs& a, const float*
       t2 = fmax(fmin(t1, o1), fmax(t2, o2));
       t1 = fmax(t1, o1);
     }
-    double mine = __shfl_sync(kAll, a.gtop == 2 ? t1 + t2 : t1, (lane << lg) & 31);  // lane g: group g's score
+    double mine = t1;
+    if (a.gtop == 2) {
+      // Scores, biases and lifts are summed each for itself: two groups whose
+      // sums are equal over the reals because they share them out differently
+      // (the same logits, one expert of each resident) are equal here too.
+      const int g0 = (lane >> lg) * m;
+      int e1 = INT_MAX, e2 = INT_MAX;  // the lowest experts with these values
+      if ((lane >> lg) < a.G)
+        for (int j = lane & (lanes - 1); j < m && e1 == INT_MAX; j += lanes)
+          if (c[g0 + j] == t1) e1 = g0 + j;
+      for (int o = lanes >> 1; o; o >>= 1) e1 = min(e1, __shfl_xor_sync(kAll, e1, o));
+      if ((lane >> lg) < a.G)
+        for (int j = lane & (lanes - 1); j < m && e2 == INT_MAX; j += lanes)
+          if (c[g0 + j] == t2 && g0 + j != e1) e2 = g0 + j;
+      for (int o = lanes >> 1; o; o >>= 1) e2 = min(e2, __shfl_xor_sync(kAll, e2, o));
+      mine = -INFINITY;  // where one of the two is off
+      if (t2 > -INFINITY && e1 < E && e2 < E) {
+        mine = __dadd_rn(__dmul_rn(score(logit(row, e1)), scale), __dmul_rn(score(logit(row, e2)), scale));
+        if (a.bias) mine = __dadd_rn(mine, __dadd_rn((double)a.bias[e1], (double)a.bias[e2]));
+        const int n = lifted ? (a.table[e1] >= 0 ? 1 : 0) + (a.table[e2] >= 0 ? 1 : 0) : 0;
+        if (n) mine = lift_of(mine, a.L, hi, lo, (double)n);
+      }
+    }
+    mine = __shfl_sync(kAll, mine, (lane << lg) & 31);  // lane g: group g's score
     int better = 0;
     for (int g = 0; g < a.G; ++g) {
       const double v = __shfl_sync(kAll, mine, g);

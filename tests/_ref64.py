@@ -44,7 +44,17 @@ def route(logits, k, sigmoid, bias=None, G=1, top=1, gtop=1, renorm=True, scale=
     for t in range(T):
         groups = range(G)
         if top < G:
-            score = [np.sort(c[t, g * m:(g + 1) * m])[::-1][:gtop].sum() for g in range(G)]
+            score = [c[t, g * m:(g + 1) * m].max() for g in range(G)]
+            for g in range(G) if gtop == 2 else ():
+                # scores, biases and lifts each for itself: what is equal over the reals is equal here
+                e1, e2 = g * m + np.argsort(-c[t, g * m:(g + 1) * m], kind="stable")[:2]
+                score[g] = -np.inf
+                if not (off[t, e1] or off[t, e2]):
+                    score[g] = s[t, e1] + s[t, e2] + (0.0 if bias is None else np.float64(bias[e1]) + np.float64(bias[e2]))
+                    n = 0 if L == 0 or not hi[t] > lo[t] else int(table[e1] >= 0) + int(table[e2] >= 0)
+                    if n:
+                        down = (np.float64(np.float32(L)) - 1.0) * (hi[t] - lo[t])
+                        score[g] = n * hi[t] + ((score[g] - n * lo[t]) + n * down)
             groups = sorted(range(G), key=lambda g: (-score[g], g))[:top]
         cand = [e for g in groups for e in range(g * m, (g + 1) * m)]
         cand.sort(key=lambda e: (-c[t, e], -l[t, e], e))

@@ -311,3 +311,16 @@ def test_full_substitution_with_equal_lowest_scores(E, k):
         logits = (np.round(synth.router_logits(9, step, 340, E) * 4) / 4).astype(np.float32)
         check(logits, k, "softmax", None, 1, 1, 1, False, 2.5, 1.0,
               np.where(r.random(E) < k / E, r.integers(0, 50, E), -1).astype(np.int32))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,G,top", [(48, 29, 16, 10), (64, 28, 32, 20), (128, 8, 16, 5), (256, 8, 32, 9)])
+def test_groups_equal_over_the_reals(score, E, k, G, top):
+    """Few distinct logits: groups' sums are often equal over the reals because
+    the same scores, lifts or biases are paired otherwise; the lower group is kept."""
+    r = np.random.default_rng(E)
+    logits = (np.round(synth.router_logits(10, 0, 300, E) * 2) / 2).astype(np.float32)
+    table = np.where(r.random(E) < 0.4, r.integers(0, 50, E), -1).astype(np.int32)
+    b = (np.round(r.standard_normal(E)) / 8).astype(np.float32)
+    check(logits, k, score, None, G, top, 2, True, 1.0, 0.125, table)
+    check(logits, k, score, b, G, top, 2, True, 1.0, 0.0, table)
