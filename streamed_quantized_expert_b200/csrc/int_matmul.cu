@@ -231,6 +231,14 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile
   }
 }
 
+// The same for a warp that goes on together: its lanes may see the barrier and
+// the flag in different orders, so they go on only if all of them may, and
+// leave together (what follows the wait has warp-wide loads and shuffles).
+__device__ __forceinline__ bool tc_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                             long long limit_cycles) {
+  return __all_sync(0xffffffffu, !*abort_flag && tc_wait(bar, parity, abort_flag, limit_cycles));
+}
+
 // 32 tokens (t.., the first `cnt` of them exist) of one output per lane, from
 // the accumulators v: y is written 128 (fp32) or 64 (bf16) contiguous bytes
 // per token and warp.  xs: the tokens' scales.  With `pairs` (N even, y
@@ -432,10 +440,10 @@ __global__ void __launch_bounds__(tc_threads(SPLIT), SPLIT ? 2 : 1)
     float* xs = s_xs[warp - kTcEpiWarp0];
     int c = 0;
     uint32_t pc = 0;
-    for (int t = tile0; t < tiles && !s_abort; t += step) {
+    for (int t = tile0; t < tiles; t += step) {
       const int n = (t % mtiles) * kTcBM + 32 * q + lane, t0 = (t / mtiles) * NB;
       const float ws = n < a.N ? a.ws[n] : 0.0f;
-      if (!tc_wait(&accfull[c], pc, &s_abort, a.wait_limit)) break;
+      if (!tc_wait_warp(&accfull[c], pc, &s_abort, a.wait_limit)) break;
       tc_fence_after();
       for (int col = 32 * part; col < NB && t0 + col < a.T; col += 8 * kEpi) {
         uint32_t v[32];
@@ -688,10 +696,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     float* xs = s_xs[warp - kTcEpiWarp0];
     int c = 0;
     uint32_t pc = 0;
-    for (int t = tile0; t < tiles && !s_abort; t += step) {
+    for (int t = tile0; t < tiles; t += step) {
       const int n = (t % mtiles) * kPairBM + 128 * (int)rank + 32 * q + lane, t0 = (t / mtiles) * kPairBN;
       const float ws = n < a.N ? a.ws[n] : 0.0f;
-      if (!tc_wait(&accfull[c], pc, &s_abort, a.wait_limit)) break;
+      if (!tc_wait_warp(&accfull[c], pc, &s_abort, a.wait_limit)) break;
       tc_fence_after();
       for (int col = 32 * part; col < kPairBN && t0 + col < a.T; col += 8 * kEpi) {
         uint32_t v[32];
