@@ -327,15 +327,55 @@ __device__ __forceinline__ void row_out(const RowQuantArgs& a, int64_t row, int 
   *reinterpret_cast<uint2*>(a.q + row * a.H + c) = coder.codes(p);
 }
 
-template <int OP>
-__device__ __forceinline__ float row_factor(const RowQuantArgs& a, float sum) {
-  return OP == kRowNorm ? rsqrtf(fmaf(sum, a.inv_h, a.eps)) : 1.0f;
+// One value of the residual: read back from h_out (the caller's own writes;
+// h_out may be the input), or summed again.
+template <bool HF32, bool DF32>
+__device__ __forceinline__ float residual_at(const RowQuantArgs& a, int64_t at) {
+  auto load = [](const void* p, bool f32, int64_t i) {
+    return f32 ? static_cast<const float*>(p)[i] : __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
+  };
+  const float h = load(a.h_out ? a.h_out : a.in, HF32, at);
+  if (a.h_out || !a.delta) return h;
+  const float sum = __fadd_rn(h, load(a.delta, DF32, at));
+  return HF32 ? sum : __uint_as_float((uint32_t)f32_to_bf16_rne(sum) << 16);
+}
+
+// The row's factor r, from the sum of its squares.  Where that left fp32's
+// range (512 squares of 1e18 do), the row is read again and summed times 2^-80,
+// whose squares stay below 2^96: a power of two, which rounds nothing else.
+// i, n: this thread and the row's threads.  One value at a time, so that rows
+// of ordinary size, which never come here, keep their registers.
+template <int OP, bool HF32, bool DF32, bool WARP>
+__device__ __forceinline__ float row_factor(const RowQuantArgs& a, int64_t row, int i, int n, float sum) {
+  if constexpr (OP != kRowNorm) return 1.0f;
+  if (sum < INFINITY) return rsqrtf(fmaf(sum, a.inv_h, a.eps));
+  constexpr float kTimes = 0x1p-80f;
+  float amax = 0.0f;
+  sum = 0.0f;
+#pragma unroll 1
+  for (int c = 8 * i; c < a.H; c += c % 8 == 7 ? 8 * n - 7 : 1) {
+    const float v = kTimes * residual_at<HF32, DF32>(a, row * a.H + c);
+    sum = fmaf(v, v, sum);
+  }
+  if (!WARP) __syncthreads();  // the first sums have been read
+  row_reduce<WARP>(sum, amax);
+  return kTimes * rsqrtf(fmaf(sum, a.inv_h, a.eps * kTimes * kTimes));
+}
+
+// Threads of a block at most, and blocks that an SM is to hold.  The norm of
+// short bf16 rows keeps 32 registers, so that its cold path costs no occupancy.
+__host__ __device__ constexpr int row_threads(int op, int ch, bool warp) {
+  return warp || (op == kRowNorm && ch == 1) ? 256 : ch == 4 ? 512 : 1024;
+}
+__host__ __device__ constexpr int row_blocks(int op, bool hf32, int ch, bool warp) {
+  return ch == 4 ? 2 : op == kRowNorm && ch == 1 ? (hf32 ? 6 : 8) : 1;
 }
 
 // Rows held in registers, CH pieces of eight columns a thread: one pass over
 // the data.  A row is a warp's (WARP: eight rows to a block) or a block's.
 template <int OP, bool HF32, bool DF32, int CH, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : CH == 4 ? 512 : 1024, CH == 4 ? 2 : 1) row_quant_kernel(const RowQuantArgs a) {
+__global__ void __launch_bounds__(row_threads(OP, CH, WARP), row_blocks(OP, HF32, CH, WARP))
+    row_quant_kernel(const RowQuantArgs a) {
   using Raw = RowRaw<OP, HF32, DF32>;
   const int n = WARP ? 32 : blockDim.x, i = WARP ? threadIdx.x & 31 : threadIdx.x;
   const int64_t row = WARP ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
@@ -364,7 +404,7 @@ __global__ void __launch_bounds__(WARP ? 256 : CH == 4 ? 512 : 1024, CH == 4 ? 2
   const float2 half = split2(sum2);
   float sum = half.x + half.y;
   row_reduce<WARP>(sum, amax);
-  const float r = row_factor<OP>(a, sum);
+  const float r = row_factor<OP, HF32, DF32, WARP>(a, row, i, n, sum);
   const RowCoder<OP != kRowSwiglu && !HF32> coder(amax);
   if (i == 0 && a.scale) a.scale[row] = scale_of(amax, r);
 #pragma unroll
@@ -394,7 +434,7 @@ __global__ void __launch_bounds__(1024) row_quant_long_kernel(RowQuantArgs a) {
   const float2 half = split2(sum2);
   float sum = half.x + half.y;
   row_reduce<false>(sum, amax);
-  const float r = row_factor<OP>(a, sum);
+  const float r = row_factor<OP, HF32, DF32, false>(a, row, threadIdx.x, blockDim.x, sum);
   const RowCoder<OP != kRowSwiglu && !HF32> coder(amax);
   if (threadIdx.x == 0 && a.scale) a.scale[row] = scale_of(amax, r);
   if (OP == kRowNorm && a.h_out) {  // from here on the residual is this thread's own writes (h_out may be the input)
