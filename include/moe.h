@@ -428,8 +428,8 @@ moe_status moe_route_grouped(const float* logits, int32_t T, const moe_layer_des
  *           or both NULL; x or q must be given
  * A row of zeros has codes and scale 0; a row with an infinity or a NaN has
  * codes 0 and scale NaN.  Squares are summed in fp32 in a fixed order
- * (deterministic), of values times a power of two where their sum would not
- * hold; |h'| below 1e18.  H a multiple of 8, at most 65536; h,
+ * (deterministic), of values times a power of two where fp32 would not hold
+ * their sum or, next to a tiny eps, the squares; |h'| below 1e18.  H a multiple of 8, at most 65536; h,
  * delta, gamma, h_out and x 16-byte aligned, q 8-byte aligned. */
 moe_status moe_add_norm_quant(const void* h, int32_t h_type, const void* delta, int32_t delta_type,
                               const uint16_t* gamma, float eps, int32_t T, int32_t H, void* h_out, uint16_t* x,

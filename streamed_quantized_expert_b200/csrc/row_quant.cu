@@ -341,25 +341,28 @@ __device__ __forceinline__ float residual_at(const RowQuantArgs& a, int64_t at) 
 }
 
 // The row's factor r, from the sum of its squares.  Where that left fp32's
-// range (512 squares of 1e18 do), the row is read again and summed times 2^-80,
-// whose squares stay below 2^96: a power of two, which rounds nothing else.
-// i, n: this thread and the row's threads.  One value at a time, so that rows
-// of ordinary size, which never come here, keep their registers.
+// range (512 squares of 1e18 do), or where next to a tiny eps the squares lost
+// bits below it (mean + eps under 2^-80, of which the 2^-150 that a square may
+// lose is more than 2^-70), the row is read again and summed times 2^-80 or
+// 2^60, whose squares stay below 2^96 and 2^56: powers of two, which round
+// nothing else.  i, n: this thread and the row's threads.  One value at a time,
+// so that ordinary rows, which never come here, keep their registers.
 template <int OP, bool HF32, bool DF32, bool WARP>
 __device__ __forceinline__ float row_factor(const RowQuantArgs& a, int64_t row, int i, int n, float sum) {
   if constexpr (OP != kRowNorm) return 1.0f;
-  if (sum < INFINITY) return rsqrtf(fmaf(sum, a.inv_h, a.eps));
-  constexpr float kTimes = 0x1p-80f;
+  const float mean = fmaf(sum, a.inv_h, a.eps);
+  if (mean >= 0x1p-80f && mean < INFINITY) return rsqrtf(mean);
+  const float times = mean < 1.0f ? 0x1p60f : 0x1p-80f;
   float amax = 0.0f;
   sum = 0.0f;
 #pragma unroll 1
   for (int c = 8 * i; c < a.H; c += c % 8 == 7 ? 8 * n - 7 : 1) {
-    const float v = kTimes * residual_at<HF32, DF32>(a, row * a.H + c);
+    const float v = times * residual_at<HF32, DF32>(a, row * a.H + c);
     sum = fmaf(v, v, sum);
   }
   if (!WARP) __syncthreads();  // the first sums have been read
   row_reduce<WARP>(sum, amax);
-  return kTimes * rsqrtf(fmaf(sum, a.inv_h, a.eps * kTimes * kTimes));
+  return times * rsqrtf(fmaf(sum, a.inv_h, a.eps * times * times));
 }
 
 // Threads of a block at most, and blocks that an SM is to hold.  The norm of
