@@ -217,12 +217,14 @@ __device__ __forceinline__ long long exit_limit(const IntMatmulArgs& a) {
 }
 
 // Bounded wait that also gives up once another role of the CTA has aborted.
+// A thread is suspended for 20 us (40,000 cycles) at most, and polls instead
+// where the limit is shorter than that.
 __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                         long long limit_cycles) {
   if (mbar_test(bar, parity)) return true;
   const long long t0 = clock64();
   for (;;) {
-    if (mbar_try_wait(bar, parity, 20000u)) return true;
+    if (limit_cycles < 40000 ? mbar_test(bar, parity) : mbar_try_wait(bar, parity, 20000u)) return true;
     if (*abort_flag) return false;
     if (clock64() - t0 > limit_cycles) {
       *abort_flag = 1;

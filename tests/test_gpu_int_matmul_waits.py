@@ -37,3 +37,20 @@ def test_limits_around_a_tile(T, N, K):
             ops.moe_set_wait_limit_cycles(0)
         assert int(err.item()) in (0, ops.DEV_ERR_TIMEOUT)
         check(run(*a, True), *a, True)
+
+
+@pytest.mark.parametrize("T,N,K", SIZES)
+def test_the_shortest_limit_runs_out(T, N, K):
+    """A limit of one cycle is shorter than a copy takes: every kernel reports
+    MOE_DEV_ERR_TIMEOUT, also where the default limit returns right after it."""
+    a = inputs(9, T, N, K, True, True)
+    b = [dev(x) for x in a]
+    y, err = torch.empty((T, N), device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    try:
+        ops.moe_set_wait_limit_cycles(1)
+        ops.moe_int_matmul(b[0], b[1], T, b[2], b[3], N, K, b[4], b[5], y, ops.MOE_F32, err)
+        torch.cuda.synchronize()
+    finally:
+        ops.moe_set_wait_limit_cycles(0)
+    assert int(err.item()) == ops.DEV_ERR_TIMEOUT
+    check(run(*a, True), *a, True)
