@@ -179,11 +179,15 @@ def _ck(status: int, where: str) -> None:
 
 def _ptr(t) -> int | None:
     """Device (or host) address of a tensor / int / None."""
-    return t if t is None or t.__class__ is int else t.data_ptr()
+    if t is None or t.__class__ is int:
+        return t
+    return int(t) if isinstance(t, int) else t.data_ptr()
 
 
 def _stream(s) -> int | None:
-    return s if s is None or s.__class__ is int else s.cuda_stream  # torch.cuda.Stream
+    if s is None or s.__class__ is int:
+        return s
+    return int(s) if isinstance(s, int) else s.cuda_stream  # torch.cuda.Stream
 
 
 def desc(E, k, H, I, group, bits_gu, bits_down=None) -> LayerDesc:
