@@ -467,6 +467,8 @@ class Streamer:
             raise ops.MoeError(ops.MOE_ERR_CAPACITY, "Streamer.block")
         if (T > 64 and not prefill) or not self._block_fits(spec, h, delta, T, row_w, y):
             raise ops.MoeError(ops.MOE_ERR_INVALID, "Streamer.block")
+        if not prefill and not 0.0 <= C.c_float(L).value <= C.c_float(1e30).value:  # as the routing takes it
+            raise ops.MoeError(ops.MOE_ERR_INVALID, "Streamer.block: L")
         if self.x is None:
             new = lambda *shape, dt: torch.empty(shape, dtype=dt, device=self.device)  # noqa: E731
             self.x = new(self.max_tokens, self.H, dt=torch.bfloat16)
