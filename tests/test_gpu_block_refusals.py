@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from streamed_quantized_expert_b200 import build, ops
-from streamed_quantized_expert_b200.runtime import Streamer
+from streamed_quantized_expert_b200.runtime import LayerSpec, Streamer
 from tests.test_gpu_layer_block import H, layers
 
 pytestmark = pytest.mark.gpu
@@ -47,3 +47,22 @@ def block(orc):
 @pytest.mark.parametrize("L", [-0.5, float("nan"), float("inf"), 2e30, 1e300])
 def test_substitution_strength(block, T, L):
     block.refused(INV, T=T, L=L)
+
+
+@pytest.mark.parametrize("T,prefill", [(1, False), (3, False), (70, True)])
+@pytest.mark.parametrize("status,change", [
+    (INV, dict(n_groups=7)), (INV, dict(n_groups=32, top_groups=2)), (INV, dict(score=5)), (INV, dict(group_top=3)),
+    (INV, dict(scale=float("nan"))), (UNS, dict(n_groups=64, top_groups=64, group_top=1))])
+def test_route_config(orc, block, status, change, T, prefill):
+    """Groups that do not divide 64 experts, 6 of 4 kept ones, and so on: refused
+    when the Streamer is made, and by a block whose layer was changed afterwards."""
+    good = block.spec.route
+    bad = ops.RouteConfig(good.score, good.n_groups, good.top_groups, good.group_top, good.renormalise, good.scale)
+    for name, v in change.items():
+        setattr(bad, name, v)
+    with pytest.raises(ops.MoeError) as ei:
+        Streamer([LayerSpec(**{**block.spec.__dict__, "route": bad})], 24, max_tokens=8)
+    assert ei.value.status == status
+    for name, v in change.items():
+        setattr(good, name, v)
+    block.refused(status, T=T, prefill=prefill)
