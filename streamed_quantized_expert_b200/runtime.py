@@ -75,12 +75,14 @@ class IntExpert:
     and up rows w_gu [2I, H] and down rows w_down [H, I] (fp32 or bf16, on the
     device) are quantised once, on `stream` (later calls on another stream wait
     for it themselves), with a scale per output; the activations take a scale
-    per token."""
+    per token.  H and I are multiples of 16 (rows of moe_int_matmul), at most 65536."""
 
     def __init__(self, w_gu: torch.Tensor, w_down: torch.Tensor, max_tokens: int,
                  stream: torch.cuda.Stream | None = None):
         self.H, self.I = w_gu.shape[1], w_gu.shape[0] // 2
         assert tuple(w_down.shape) == (self.H, self.I) and w_gu.shape[0] == 2 * self.I
+        if self.H < 16 or self.I < 16 or self.H % 16 or self.I % 16:
+            raise ops.MoeError(ops.MOE_ERR_INVALID, f"IntExpert of {self.H} x {self.I}: multiples of 16")
         dev = w_gu.device
         self.max_tokens = max_tokens
         st = stream or torch.cuda.current_stream(dev)

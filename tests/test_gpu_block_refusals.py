@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from streamed_quantized_expert_b200 import build, ops
-from streamed_quantized_expert_b200.runtime import LayerSpec, Streamer
+from streamed_quantized_expert_b200.runtime import IntExpert, LayerSpec, Streamer
 from tests.test_gpu_layer_block import H, layers
 
 pytestmark = pytest.mark.gpu
@@ -66,3 +66,21 @@ def test_route_config(orc, block, status, change, T, prefill):
     for name, v in change.items():
         setattr(good, name, v)
     block.refused(status, T=T, prefill=prefill)
+
+
+@pytest.mark.parametrize("width", [8, 24, 200])
+def test_width_of_an_integer_expert(width):
+    """The products take K in multiples of 16, the codes in multiples of 8."""
+    with pytest.raises(ops.MoeError) as ei:
+        IntExpert(torch.ones((2 * width, H), device="cuda"), torch.ones((H, width), device="cuda"), 4)
+    assert ei.value.status == INV
+    with pytest.raises(ops.MoeError) as ei:
+        IntExpert(torch.ones((64, width), device="cuda"), torch.ones((width, 32), device="cuda"), 4)
+    assert ei.value.status == INV
+
+
+def test_integer_expert_too_wide():
+    wide = (1 << 16) + 16
+    with pytest.raises(ops.MoeError) as ei:
+        IntExpert(torch.ones((2 * wide, 16), device="cuda"), torch.ones((16, wide), device="cuda"), 4)
+    assert ei.value.status == UNS
