@@ -453,6 +453,7 @@ class Streamer:
         return (gamma is not None and router is not None
                 and gamma.numel() == self.H and holds(gamma, self.H, *bits)
                 and tuple(router.shape) == (self.E, self.H) and holds(router, 0, *bits)
+                and router.data_ptr() % 16 == 0  # as moe_router_logits reads it
                 and holds(h, n, torch.float32, *bits)
                 and (delta is None or holds(delta, n, torch.float32, *bits))
                 and (row_w is None or holds(row_w, T, torch.float32))

@@ -84,3 +84,11 @@ def test_integer_expert_too_wide():
     with pytest.raises(ops.MoeError) as ei:
         IntExpert(torch.ones((2 * wide, 16), device="cuda"), torch.ones((16, wide), device="cuda"), 4)
     assert ei.value.status == UNS
+
+
+@pytest.mark.parametrize("T", [1, 3, 70])
+def test_alignment_of_the_router(block, T):
+    E = block.st.E
+    odd = torch.zeros(E * H + 8, dtype=torch.bfloat16, device="cuda")[1:E * H + 1].view(E, H)
+    block.spec.router = odd
+    block.refused(INV, T=T)
