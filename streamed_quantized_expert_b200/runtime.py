@@ -478,6 +478,8 @@ class Streamer:
             raise ops.MoeError(ops.MOE_ERR_CAPACITY, "Streamer.block")
         if (T > 64 and not prefill) or not self._block_fits(spec, h, delta, T, row_w, y):
             raise ops.MoeError(ops.MOE_ERR_INVALID, "Streamer.block")
+        if T > 65535:  # as moe_router_logits takes them
+            raise ops.MoeError(ops.MOE_ERR_UNSUPPORTED, "Streamer.block")
         self._check_route(spec)
         if not prefill and not 0.0 <= C.c_float(L).value <= C.c_float(1e30).value:  # as the routing takes it
             raise ops.MoeError(ops.MOE_ERR_INVALID, "Streamer.block: L")

@@ -92,3 +92,9 @@ def test_alignment_of_the_router(block, T):
     odd = torch.zeros(E * H + 8, dtype=torch.bfloat16, device="cuda")[1:E * H + 1].view(E, H)
     block.spec.router = odd
     block.refused(INV, T=T)
+
+
+def test_tokens_beyond_the_router(orc):
+    block = Block(orc, 65536)
+    block.spec.always = None
+    block.refused(UNS, T=65536)
