@@ -83,7 +83,7 @@ class IntExpert:
         assert tuple(w_down.shape) == (self.H, self.I) and w_gu.shape[0] == 2 * self.I
         if self.H < 16 or self.I < 16 or self.H % 16 or self.I % 16:
             raise ops.MoeError(ops.MOE_ERR_INVALID, f"IntExpert of {self.H} x {self.I}: multiples of 16")
-        dev = w_gu.device
+        dev = self.device = w_gu.device
         self.max_tokens = max_tokens
         st = stream or torch.cuda.current_stream(dev)
 
@@ -444,10 +444,10 @@ class Streamer:
 
     def _block_fits(self, spec, h, delta, T: int, row_w, y) -> bool:
         """Whether block can read and write all that it is given."""
-        bits = (torch.bfloat16, torch.int16, torch.uint16)
+        bits, here = (torch.bfloat16, torch.int16, torch.uint16), self.dev_err.device
 
         def holds(t, n, *types):
-            return t.is_cuda and t.is_contiguous() and t.numel() >= n and t.dtype in types
+            return t.device == here and t.is_contiguous() and t.numel() >= n and t.dtype in types
 
         n, gamma, router = T * self.H, spec.norm, spec.router
         return (gamma is not None and router is not None
@@ -458,7 +458,7 @@ class Streamer:
                 and (delta is None or holds(delta, n, torch.float32, *bits))
                 and (row_w is None or holds(row_w, T, torch.float32))
                 and (y is None or holds(y, n, torch.float32))
-                and (spec.always is None or spec.always.H == self.H))
+                and (spec.always is None or (spec.always.H == self.H and spec.always.device == here)))
 
     def block(self, layer: int, h: torch.Tensor, delta, T: int, L: float = 0.0, eps: float = 1e-6, prefill=None,
               row_w=None, y=None):
