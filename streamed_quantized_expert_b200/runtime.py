@@ -490,6 +490,8 @@ class Streamer:
             self.x_scale = new(self.max_tokens, dt=torch.float32)
             self.logits = new(self.max_tokens, self.E, dt=torch.float32)
             s.wait_stream(torch.cuda.current_stream(self.device))  # the buffers' memory comes from there
+        if y is not None:  # the first T rows: prefill_layer zeroes all that it is given
+            y = y.view(-1)[:T * self.H].view(T, self.H)
         codes = always is not None
         ops.moe_add_norm_quant(h, _kind(h), delta, ops.MOE_BF16 if delta is None else _kind(delta), spec.norm, eps, T,
                                self.H, h if delta is not None else None, self.x, self.xq if codes else None,

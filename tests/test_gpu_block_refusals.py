@@ -98,3 +98,16 @@ def test_tokens_beyond_the_router(orc):
     block = Block(orc, 65536)
     block.spec.always = None
     block.refused(UNS, T=65536)
+
+
+@pytest.mark.parametrize("T", [1, 3, 70])
+def test_rows_of_y_behind_the_last_token(orc, T):
+    """y may hold more rows: those behind the last token stay as they were."""
+    st, _, _ = layers(orc, 1, 64)
+    h = torch.randn((T, H), device="cuda").bfloat16()
+    y = torch.full((T + 3, H), 7.0, device="cuda")
+    got = st.block(0, h.clone(), None, T, y=y)
+    want = st.block(0, h.clone(), None, T)
+    torch.cuda.synchronize()
+    assert (y[T:] == 7).all() and tuple(got.shape) == (T, H)
+    assert torch.equal(y[:T], want[:T]) and got.data_ptr() == y.data_ptr()
