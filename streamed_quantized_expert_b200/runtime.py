@@ -126,7 +126,9 @@ class Streamer:
         self.k = layers[0].desc.k
         self.H = layers[0].desc.H
         assert all(l.desc.E == self.E and l.desc.H == self.H for l in layers)
+        here = torch.empty(0, device=self.device).device  # with its index
         assert all(l.route_bias is None or (l.route is not None and l.route_bias.dtype == torch.float32
+                                            and l.route_bias.device == here
                                             and l.route_bias.is_contiguous() and l.route_bias.numel() == self.E)
                    for l in layers)
         for l in layers:

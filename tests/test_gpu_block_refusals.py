@@ -111,3 +111,11 @@ def test_rows_of_y_behind_the_last_token(orc, T):
     torch.cuda.synchronize()
     assert (y[T:] == 7).all() and tuple(got.shape) == (T, H)
     assert torch.equal(y[:T], want[:T]) and got.data_ptr() == y.data_ptr()
+
+
+def test_bias_on_the_host(orc):
+    """The routing kernels read the bias: it has to be on the Streamer's device."""
+    st, _, _ = layers(orc, 1, 24)
+    spec = st.layers[0]
+    with pytest.raises(AssertionError):
+        Streamer([LayerSpec(**{**spec.__dict__, "route_bias": spec.route_bias.cpu()})], 24, max_tokens=8)
