@@ -202,6 +202,7 @@ class Streamer:
                                      self.x_sorted.data_ptr() if self.x_sorted is not None else None)
         self._ctx = []
         self._rows = []
+        self._biases = [spec.route_bias for spec in layers]  # the contexts hold their addresses
         for l, spec in enumerate(layers):
             rows = (C.c_void_p * self.E)(*[self._row_addr(l, e) for e in range(self.E)])
             self._rows.append(rows)

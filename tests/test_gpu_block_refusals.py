@@ -1,5 +1,8 @@
 """What Streamer.block refuses leaves h (and y) as it was, so that the caller can correct
 the call and make it again: arguments that only a later stage would refuse."""
+import gc
+import weakref
+
 import pytest
 import torch
 
@@ -119,3 +122,12 @@ def test_bias_on_the_host(orc):
     spec = st.layers[0]
     with pytest.raises(AssertionError):
         Streamer([LayerSpec(**{**spec.__dict__, "route_bias": spec.route_bias.cpu()})], 24, max_tokens=8)
+
+
+def test_a_bias_lives_as_long_as_the_streamer(orc):
+    """The native driver keeps the bias's address: a LayerSpec that is changed afterwards does not free it."""
+    st, _, _ = layers(orc, 1, 24)
+    bias = weakref.ref(st.layers[0].route_bias)
+    st.layers[0].route_bias = None
+    gc.collect()
+    assert bias() is not None and bias().data_ptr() == st._ctx[0].route_bias
