@@ -131,9 +131,9 @@ class Streamer:
                                             and l.route_bias.device == here
                                             and l.route_bias.is_contiguous() and l.route_bias.numel() == self.E)
                    for l in layers)
+        self.ns = n_shared
         for l in layers:
             self._check_route(l)
-        self.ns = n_shared
         assert n_shared == 0 or all(l.shared is not None and l.shared.shape[0] == n_shared for l in layers)
         self.Ew, self.kw = self.E + n_shared, self.k + n_shared  # the widened layer
         self.wdesc = [ops.widened(l.desc, n_shared) for l in layers]
@@ -224,11 +224,12 @@ class Streamer:
         self.g_ids_pin = torch.empty(2 * stride, dtype=torch.int32).pin_memory()
         self._gbufs = ops.GuessBuffers(self.g_ids.data_ptr(), self.g_w.data_ptr(), self.g_ids_pin.data_ptr(), stride)
 
-    @staticmethod
-    def _check_route(spec: LayerSpec) -> None:
-        """Raises what moe_route_grouped would refuse of the layer's own routing (no tokens: nothing runs)."""
+    def _check_route(self, spec: LayerSpec) -> None:
+        """Raises what the routing would refuse of the layer (no tokens: nothing runs)."""
         if spec.route is not None:
-            ops.moe_route_grouped(None, 0, spec.desc, spec.route, None, 0.0, None, 0, None, None, None)
+            ops.moe_route_grouped(None, 0, spec.desc, spec.route, None, 0.0, None, self.ns, None, None, None)
+        else:
+            ops.moe_route_shared(None, 0, spec.desc, 0.0, None, self.ns, None, None, None)
 
     # -- views into meta --------------------------------------------------
     def _n_active(self):
@@ -481,7 +482,8 @@ class Streamer:
             raise ops.MoeError(ops.MOE_ERR_CAPACITY, "Streamer.block")
         if (T > 64 and not prefill) or not self._block_fits(spec, h, delta, T, row_w, y):
             raise ops.MoeError(ops.MOE_ERR_INVALID, "Streamer.block")
-        if T > 65535:  # as moe_router_logits takes them
+        # as moe_router_logits and the experts' FFN take them
+        if T > 65535 or ops.moe_ffn_kernel_path(self.wdesc[layer], T, True) < 0:
             raise ops.MoeError(ops.MOE_ERR_UNSUPPORTED, "Streamer.block")
         self._check_route(spec)
         if not prefill and not 0.0 <= C.c_float(L).value <= C.c_float(1e30).value:  # as the routing takes it

@@ -131,3 +131,26 @@ def test_a_bias_lives_as_long_as_the_streamer(orc):
     st.layers[0].route_bias = None
     gc.collect()
     assert bias() is not None and bias().data_ptr() == st._ctx[0].route_bias
+
+
+@pytest.mark.parametrize("T", [1, 3, 70])
+@pytest.mark.parametrize("kw,ns", [(dict(k=31, bits=4), 2), (dict(k=4, bits=16), 0)])
+def test_experts_that_cannot_run(kw, ns, T):
+    """33 experts a token with the shared ones; BF16 experts whose width the tensor-core path does not take."""
+    d = ops.desc(64, kw["k"], H, 96, 32, kw["bits"])
+    bank = torch.zeros((64, ops.moe_slot_bytes(d)), dtype=torch.uint8).pin_memory()
+    block = Block.__new__(Block)
+    block.st = Streamer([LayerSpec(d, bank, list(range(64)), shared=bank[:ns] if ns else None,
+                                   norm=torch.ones(H, dtype=torch.bfloat16, device="cuda"),
+                                   router=torch.zeros((64, H), dtype=torch.bfloat16, device="cuda"))],
+                        64, max_tokens=128, n_shared=ns)
+    block.refused(UNS, T=T)
+
+
+@pytest.mark.parametrize("route", [None, ops.route_config("sigmoid", 8, 4, 2)])
+def test_more_shared_experts_than_the_routing_takes(route):
+    d = ops.desc(64, 4, H, 128, 32, 4)
+    bank = torch.zeros((64, ops.moe_slot_bytes(d)), dtype=torch.uint8).pin_memory()
+    with pytest.raises(ops.MoeError) as ei:
+        Streamer([LayerSpec(d, bank, list(range(64)), shared=bank[:9], route=route)], 64, max_tokens=8, n_shared=9)
+    assert ei.value.status == INV
