@@ -75,7 +75,12 @@ class IntExpert:
     and up rows w_gu [2I, H] and down rows w_down [H, I] (fp32 or bf16, on the
     device) are quantised once, on `stream` (later calls on another stream wait
     for it themselves), with a scale per output; the activations take a scale
-    per token.  H and I are multiples of 16 (rows of moe_int_matmul), at most 65536."""
+    per token.  H and I are multiples of 16 (rows of moe_int_matmul), at most 65536.
+
+    Calls may run at once on different streams and in different graphs: each
+    stream has its own gate, up and codes, and a call that torch.cuda.graph
+    captures takes them from that graph's memory (a capture made in another way
+    takes its stream's).  gu, hq and hs are those of the last call."""
 
     def __init__(self, w_gu: torch.Tensor, w_down: torch.Tensor, max_tokens: int,
                  stream: torch.cuda.Stream | None = None):
@@ -98,21 +103,39 @@ class IntExpert:
 
         self.gu_q, self.gu_s = quantize(w_gu)
         self.down_q, self.down_s = quantize(w_down)
-        self.gu = torch.empty((max_tokens, 2 * self.I), dtype=torch.bfloat16, device=dev)
-        self.hq = torch.empty((max_tokens, self.I), dtype=torch.int8, device=dev)
-        self.hs = torch.empty(max_tokens, dtype=torch.float32, device=dev)
+        self.gu, self.hq, self.hs = first = self._new_scratch(max_tokens)
+        self._scratch = {None: first}  # by stream; the first stream to call takes None's
 
     LAUNCHES = 3
+
+    def _new_scratch(self, tokens: int):
+        return (torch.empty((tokens, 2 * self.I), dtype=torch.bfloat16, device=self.device),
+                torch.empty((tokens, self.I), dtype=torch.int8, device=self.device),
+                torch.empty(tokens, dtype=torch.float32, device=self.device))
+
+    def _scratch_for(self, T: int, stream):
+        """Gate and up, codes and scales of a call on `stream`."""
+        handle = ops._stream(stream) or 0
+        captured = torch.cuda.is_current_stream_capturing()
+        kept = None if captured else self._scratch.get(handle) or self._scratch.pop(None, None)
+        if kept is None:
+            with torch.cuda.stream(torch.cuda.ExternalStream(handle, self.device) if handle
+                                   else torch.cuda.default_stream(self.device)):
+                kept = self._new_scratch(T if captured else self.max_tokens)
+        if not captured:
+            self._scratch[handle] = kept
+        return kept
 
     def add(self, xq, x_scale, T: int, y, dev_err, row_w=None, stream=None) -> None:
         """y [T, H] (fp32) += row_w[t] (1 without) x the expert's output for
         tokens given as codes and scales (moe_add_norm_quant)."""
         if T > self.max_tokens:
             raise ops.MoeError(ops.MOE_ERR_CAPACITY, "IntExpert.add")
-        ops.moe_int_matmul(xq, x_scale, T, self.gu_q, self.gu_s, 2 * self.I, self.H, None, None, self.gu,
-                           ops.MOE_BF16, dev_err, stream)
-        ops.moe_swiglu_quant(self.gu, ops.MOE_BF16, T, self.I, self.hq, self.hs, stream)
-        ops.moe_int_matmul(self.hq, self.hs, T, self.down_q, self.down_s, self.H, self.I, y, row_w, y, ops.MOE_F32,
+        gu, hq, hs = self.gu, self.hq, self.hs = self._scratch_for(T, stream)
+        ops.moe_int_matmul(xq, x_scale, T, self.gu_q, self.gu_s, 2 * self.I, self.H, None, None, gu, ops.MOE_BF16,
+                           dev_err, stream)
+        ops.moe_swiglu_quant(gu, ops.MOE_BF16, T, self.I, hq, hs, stream)
+        ops.moe_int_matmul(hq, hs, T, self.down_q, self.down_s, self.H, self.I, y, row_w, y, ops.MOE_F32,
                            dev_err, stream)
 
 
