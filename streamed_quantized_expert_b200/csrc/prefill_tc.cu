@@ -205,6 +205,15 @@ __device__ __forceinline__ bool pf_wait(uint64_t* bar, uint32_t parity, volatile
   }
 }
 
+// Limit of the waits for a CTA's own copies and MMAs before it exits: those
+// end within microseconds, so a lowered limit does not cut them short.
+__device__ __forceinline__ long long pf_exit_limit(long long limit) { return limit > (1ll << 24) ? limit : 1ll << 24; }
+
+// For warps that go on together: the lanes may see a barrier and the flag in
+// different orders, so they go on only if all of them may, and leave together
+// (what follows a wait has warp-wide TMEM accesses and shuffles).
+__device__ __forceinline__ bool pf_all(bool ok) { return __all_sync(0xffffffffu, ok); }
+
 // BF16 experts: K quarter cq of row r from the stage's two 64-input halves
 // (128 rows x 128 bytes each, 128-byte swizzle: 16-byte chunk c of row r sits
 // at chunk c ^ (r % 8)), converted to fp16 pairs (pair index = TMEM column).
@@ -449,7 +458,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       }
       // every copy issued lands before the CTA can exit
       for (int q = 0; q < kPfStages; ++q)
-        if ((issued >> q) & 1u) mbar_wait_bounded(&full[q], (last_ph >> q) & 1u, a.wait_limit);
+        if ((issued >> q) & 1u) mbar_wait_bounded(&full[q], (last_ph >> q) & 1u, pf_exit_limit(a.wait_limit));
     }
   } else if (warp == kPfMmaWarp) {
     // ---------------- MMA issuer ----------------
@@ -502,7 +511,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       }
       if (issued_any) {  // every MMA issued completes before TMEM is freed
         umma_commit(drain);
-        mbar_wait_bounded(drain, 0, a.wait_limit);
+        mbar_wait_bounded(drain, 0, pf_exit_limit(a.wait_limit));
       }
     }
   } else if (warp < kPfDqWarps) {
@@ -516,13 +525,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     constexpr bool kRowGroups = B != 16;
     const int q = warp & 3, sel = warp >> 2, r = 32 * q + lane;
     int b = 0;  // position in the CTA's block sequence
-    for (int t = blockIdx.x; t < ntiles && !s_abort; t += gridDim.x) {
+    for (int t = blockIdx.x; t < ntiles; t += gridDim.x) {
       bool ok = true;
       for (int kb = 0; kb < a.nkb; ++kb, ++b) {
         if (kRowGroups && (b & (kPfABufs - 1)) != sel) continue;
         const int s = b % kPfStages, ab = b & (kPfABufs - 1);
         const uint32_t ph = (uint32_t)((b / kPfStages) & 1), pa = (uint32_t)((b / kPfABufs) & 1);
-        if (!pf_wait(&full[s], ph, &s_abort, a.wait_limit) || !pf_wait(&aempty[ab], pa ^ 1u, &s_abort, a.wait_limit)) {
+        if (!pf_all(pf_wait(&full[s], ph, &s_abort, a.wait_limit) &&
+                    pf_wait(&aempty[ab], pa ^ 1u, &s_abort, a.wait_limit))) {
           ok = false;
           break;
         }
@@ -544,9 +554,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const int q = warp & 3, r = 32 * q + lane, eh = (warp - kPfEpiWarp0) >> 2;  // quadrant, row, chunk parity
     int c = 0, ent_hint = 0;
     uint32_t pc = 0;
-    for (int t = blockIdx.x; t < ntiles && !s_abort; t += gridDim.x) {
+    for (int t = blockIdx.x; t < ntiles; t += gridDim.x) {
       const PfTile tl = tile_at(t, ent_hint);
-      if (!pf_wait(&accfull[c], pc, &s_abort, a.wait_limit)) break;
+      if (!pf_all(pf_wait(&accfull[c], pc, &s_abort, a.wait_limit))) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(c * NB);
       // the tile's pair indices (down) in registers: lane l holds columns l, 32 + l, ...
