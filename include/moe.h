@@ -394,7 +394,8 @@ typedef struct {
  *   the top_groups groups by the sum of their group_top best c are kept
  *   ids: the k best of the kept groups by (c desc, l desc, e asc)
  *   w_j = scale s_e, or scale s_e / sum of the chosen s (renormalise; 0 where
- *     that sum is 0)
+ *     that sum is 0 in 64 bits: sigmoids of logits below -709, or a softmax's
+ *     terms e^-745 below its largest)
  * The choice is made in 64-bit arithmetic or proved equal to it.  c, or sums of
  * a group, that lie within a few steps of 64 bits of one another may go either
  * way, unless their logits, biases and lifts are the same: then they are equal.
@@ -429,8 +430,9 @@ moe_status moe_route_grouped(const float* logits, int32_t T, const moe_layer_des
  * A row of zeros has codes and scale 0; a row with an infinity or a NaN has
  * codes 0 and scale NaN.  Squares are summed in fp32 in a fixed order
  * (deterministic), of values times a power of two where fp32 would not hold
- * their sum or, next to a tiny eps, the squares; |h'| below 1e18.  H a multiple of 8, at most 65536; h,
- * delta, gamma, h_out and x 16-byte aligned, q 8-byte aligned. */
+ * their sum or, next to a tiny eps, the squares; |h'| below 1e18.  x is made as
+ * (h' gamma) r, h' gamma in fp32.  H a multiple of 8, at most 65536; h, delta,
+ * gamma, h_out and x 16-byte aligned, q 8-byte aligned. */
 moe_status moe_add_norm_quant(const void* h, int32_t h_type, const void* delta, int32_t delta_type,
                               const uint16_t* gamma, float eps, int32_t T, int32_t H, void* h_out, uint16_t* x,
                               int8_t* q, float* q_scale, cudaStream_t stream);
@@ -459,7 +461,9 @@ moe_status moe_swiglu_quant(const void* gu, int32_t gu_type, int32_t T, int32_t 
 /* Product of 8-bit integer rows with a scale per token and per output:
  *   y[t][n] = add[t][n] + row_w[t] x_scale[t] w_scale[n] sum_k xq[t][k] wq[n][k]
  * The sum is accumulated in int32, exactly; the rest is fp32, rounded once
- * more where y is bf16.
+ * more where y is bf16.  The scales are multiplied with one another first
+ * (x_scale row_w, then w_scale): their product has to be a number that fp32
+ * holds.
  *   xq, x_scale  device int8 [T, K], 16-byte aligned, and fp32 [T]
  *   wq, w_scale  device int8 [N, K], 16-byte aligned, and fp32 [N]
  *   add          device fp32 [T, N] or NULL; may be y where y is fp32 (an

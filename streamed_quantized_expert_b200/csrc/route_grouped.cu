@@ -9,21 +9,26 @@
 // It is first made in fp32, with a bound D on how far any c may be off: where
 // every pair of neighbours among the k + 1 best, and the lowest kept and the
 // highest dropped group, are further apart than the bounds allow, the fp32
-// choice is the choice over reals.  Otherwise (about one token in a thousand
-// of N(0, 1) logits with a bias) the token is chosen again in 64 bits.  Without
-// bias and substitution the order is the logits' own, which needs no bound.
+// choice is the choice over reals.  Otherwise (about one token in six thousand
+// of N(0, 1) logits with a bias: 256 experts, 4 of 8 groups) its candidates, or
+// where the groups are in doubt all its experts, are compared again in 64 bits.
+// Without bias and substitution the order is the logits' own, which needs no
+// bound.
 //
 // One warp per token, lane i holding experts i, 32 + i, ...  The k + 1 best are
 // found through a threshold: the (k + 1)-th largest of the 32 lanes' own
 // maxima has at least k + 1 experts at or above it, and few more; those are
 // ranked by counting.
 //
-// What bounds it: instructions, 545 a token of 512 experts (its 2 KB would take
-// 0.3 ns at 6.6 TB/s), and for a few thousand tokens their latency.  16384
-// tokens x 512 experts, softmax, k 10: 13.4 us; 4096 x 256, sigmoid with bias
-// and 4 of 8 groups, k 8: 7.7 us; one token of 512 with all of it: 4.2 us
-// (243, 53 and 41 us where every score and choice is made in 64 bits with a
-// search of all experts per rank).
+// What bounds it: a warp's chain of dependent instructions (545 a token of 512
+// plain experts, 980 of 256 with bias and groups), at 2.0 to 2.6 of 4 issue
+// slots a cycle; the bytes would take 0.3 ns a token at 6.6 TB/s.  16384 tokens
+// x 512 experts, softmax, k 10: 13.4 us.  4096 x 256, sigmoid with bias and 4
+// of 8 groups, k 8, one wave that lasts as long as its slowest warp: 6.8 us
+// where no token goes to 64 bits, 8.4 on the average of N(0, 1) logits (0.7 of
+// a call's tokens go there).  One token of 512 with all of it: 4.1 us (243, 53
+// and 41 us where every score and choice is made in 64 bits with a search of
+// all experts per rank); with its sort and slot lookup in the launch 7.3.
 #include <cfloat>
 #include <climits>
 

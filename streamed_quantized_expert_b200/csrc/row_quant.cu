@@ -207,9 +207,10 @@ __device__ __forceinline__ float exp2_of(float x) {
 // whose denominator never overflows; the quotient is corrected once, which
 // leaves one rounding.  s = 2^(t + e): t = -|g| log2 e rounded, e what the
 // rounding and the constant's tail leave out, 2^e = 1 + e ln 2 (e < 2^-15).
-// |g| above 128 gives 0 like 128 does.  24 instructions a value with its code
-// bound the call: 4000 x 8200 bf16 takes 37-41 us, 4.0-4.4 TB/s (two lanes to
-// an instruction).
+// |g| above 128 gives 0 like 128 does.  24 instructions a value with its code,
+// two lanes to an instruction, are 22 us of issue at 4000 x 8200; at 27 warps an
+// SM, which all load, meet a barrier and then code, 2.5 of 4 slots issue: bf16
+// takes 38-41 us (4.0-4.3 TB/s), fp32 73 us (4.0 TB/s).
 __device__ __forceinline__ F2 swiglu_of(F2 g2, F2 u) {
   const float2 g = split2(g2);
   const F2 m = pack2(fminf(fabsf(g.x), 128.0f), fminf(fabsf(g.y), 128.0f)), one = pack2(1.0f, 1.0f);
@@ -469,8 +470,9 @@ RowPlan row_plan_of(int threads) {
 // rows there are.  Short rows are a warp's.  More pieces a thread mean fewer
 // threads at a row's barrier and more loads on the way, but a longer wait for
 // a single row: 16384 x 4096 bf16 + bf16 takes 90.0 / 89.0 / 90.3 us with 1 /
-// 2 / 4 pieces, one row of it 1.7 / 1.9 / 2.4; 4096 x 7168 plain bf16 29.1 /
-// 20.6 / 17.4, fp32 49.8 / 29.0 / 34.8.
+// 2 / 4 pieces, one row of it 1.7 / 1.9 / 2.4, 16384 x 4104 99.5 / 92.6 with 2 /
+// 4, 8192 x 7168 90.9 / 79.6; 4096 x 7168 plain bf16 29.1 / 20.6 / 17.4, fp32
+// 49.8 / 29.0 / 34.8.
 template <int OP, bool HF32, bool DF32>
 RowPlan row_plan(int H) {
   constexpr int kLong = OP == kRowNorm ? 2048 : 1024;  // one piece a thread up to here

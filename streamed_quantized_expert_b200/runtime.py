@@ -76,6 +76,8 @@ class IntExpert:
     device) are quantised once, on `stream` (later calls on another stream wait
     for it themselves), with a scale per output; the activations take a scale
     per token.  H and I are multiples of 16 (rows of moe_int_matmul), at most 65536.
+    Gate and up are kept in bf16 between the product and SwiGLU: half the bytes,
+    and their rounding (2^-8) is below that of the 8-bit codes they become.
 
     Calls may run at once on different streams and in different graphs: each
     stream has its own gate, up and codes, and a call that torch.cuda.graph
