@@ -80,9 +80,9 @@ class IntExpert:
     and their rounding (2^-8) is below that of the 8-bit codes they become.
 
     Calls may run at once on different streams and in different graphs: each
-    stream has its own gate, up and codes, and a call that torch.cuda.graph
-    captures takes them from that graph's memory (a capture made in another way
-    takes its stream's).  gu, hq and hs are those of the last call."""
+    stream has its own gate, up and codes, and a captured call takes them from
+    its graph's memory (torch.cuda.graph's; captures that torch's allocator does
+    not know of are not for add).  gu, hq and hs are those of the last call."""
 
     def __init__(self, w_gu: torch.Tensor, w_down: torch.Tensor, max_tokens: int,
                  stream: torch.cuda.Stream | None = None):
